@@ -11,6 +11,7 @@ SO = os.path.join(PKG, "libftm.so")
 FTM_OK, FTM_ERR_INVALID_ARG, FTM_ERR_UNSUPPORTED, FTM_ERR_CAPACITY, FTM_ERR_CUDA = range(5)
 FTM_F32, FTM_BF16, FTM_FP8_E4M3_B128, FTM_NVFP4, FTM_MXFP4 = range(5)
 (FTM_K_ROUTE, FTM_K_PERMUTE, FTM_K_LRU, FTM_K_GATHER, FTM_K_GEMM1, FTM_K_GEMM2, FTM_K_COMBINE) = range(7)
+FTM_ACT_SILU, FTM_ACT_GELU_TANH = range(2)
 KERNEL_NAMES = ("route", "permute", "lru", "gather", "gemm1", "gemm2", "combine")
 _WDTYPE = {"f32": FTM_F32, "bf16": FTM_BF16, "fp8": FTM_FP8_E4M3_B128, "nvfp4": FTM_NVFP4, "mxfp4": FTM_MXFP4}
 
@@ -45,6 +46,11 @@ class Hybrid(ctypes.Structure):
     _fields_ = [("pcie_gbs", ctypes.c_double), ("host_gbs", ctypes.c_double), ("threads", c_i32),
                 ("last_misses", c_i32), ("last_host", c_i32), ("last_host_rows", c_i32),
                 ("last_host_ms", ctypes.c_double), ("host_ws", c_p), ("host_ws_bytes", c_sz)]
+
+
+class LoraDesc(ctypes.Structure):
+    _fields_ = [("d_in", c_i32), ("d_out", c_i32), ("n_adapters", c_i32), ("rank", c_i32), ("wdtype", c_i32),
+                ("reserved", c_i32)]
 
 
 class FtmError(RuntimeError):
@@ -106,6 +112,17 @@ def library() -> ctypes.CDLL:
         L.ftm_host_expert_ffn.argtypes = [P(LayerDesc), c_p, c_p, c_i32, c_p, c_p, c_p, c_sz, c_i32]
         L.ftm_moe_layer_forward_hybrid.argtypes = [P(LayerDesc), P(LayerWeights), P(SlotCache), P(Hybrid), c_p,
                                                    c_i32, c_p, c_p, c_sz, c_p, c_p]
+        for name in ("ftm_gated_ffn_workspace_bytes", "ftm_gated_ffn_backward_workspace_bytes"):
+            getattr(L, name).argtypes = [P(LayerDesc), c_i32]
+            getattr(L, name).restype = c_sz
+        L.ftm_lora_workspace_bytes.argtypes = [P(LoraDesc), c_i32]
+        L.ftm_lora_workspace_bytes.restype = c_sz
+        L.ftm_gated_ffn.argtypes = [P(LayerDesc), c_i32, c_p, c_i32, c_p, c_p, c_p, c_p, c_sz, c_p]
+        L.ftm_gated_ffn_backward.argtypes = [P(LayerDesc), c_i32, c_p, c_i32, c_p, c_p, c_p, c_p, c_p, c_p, c_sz, c_p]
+        L.ftm_lora_linear.argtypes = [P(LoraDesc), c_p, c_i64, c_i32, c_p, c_p, c_p, c_p, c_p, c_p, c_i64, c_p, c_sz,
+                                      c_p]
+        for name in ("ftm_gated_ffn", "ftm_gated_ffn_backward", "ftm_lora_linear"):
+            getattr(L, name).restype = c_i32
         for name in ("ftm_get_bank_layout", "ftm_route", "ftm_permute", "ftm_slot_lookup_update", "ftm_slot_resize",
                      "ftm_slot_stage_layer", "ftm_expert_ffn", "ftm_combine", "ftm_moe_layer_forward",
                      "ftm_moe_layers_forward", "ftm_host_expert_ffn", "ftm_moe_layer_forward_hybrid"):
@@ -302,3 +319,36 @@ def ftm_moe_layer_forward_hybrid(desc, weights: LayerWeights, cache: SlotCache, 
     _check(library().ftm_moe_layer_forward_hybrid(ctypes.byref(desc), ctypes.byref(weights), ctypes.byref(cache),
                                                   ctypes.byref(hybrid), _ptr(x), T, _ptr(out), _ptr(workspace),
                                                   ws_bytes, _stream(stream), _stream(copy_stream)))
+
+
+def ftm_gated_ffn_workspace_bytes(desc, T) -> int:
+    return int(library().ftm_gated_ffn_workspace_bytes(ctypes.byref(desc), T))
+
+
+def ftm_gated_ffn(desc, act: int, x, T, bank, pre, y, workspace, ws_bytes, stream=None):
+    """The dense gated feed-forward block; pre: device bf16 [T][2I] that keeps g and u for the backward pass, or None."""
+    _check(library().ftm_gated_ffn(ctypes.byref(desc), act, _ptr(x), T, _ptr(bank), _ptr(pre), _ptr(y),
+                                   _ptr(workspace), ws_bytes, _stream(stream)))
+
+
+def ftm_gated_ffn_backward_workspace_bytes(desc, T) -> int:
+    return int(library().ftm_gated_ffn_backward_workspace_bytes(ctypes.byref(desc), T))
+
+
+def ftm_gated_ffn_backward(desc, act: int, x, T, bank, pre, dy, dx, dbank, workspace, ws_bytes, stream=None):
+    """dx / dbank: device bf16 outputs, either may be None (no gradient of the input / of the weights)."""
+    _check(library().ftm_gated_ffn_backward(ctypes.byref(desc), act, _ptr(x), T, _ptr(bank), _ptr(pre), _ptr(dy),
+                                            _ptr(dx), _ptr(dbank), _ptr(workspace), ws_bytes, _stream(stream)))
+
+
+def ftm_lora_workspace_bytes(desc: LoraDesc, T) -> int:
+    return int(library().ftm_lora_workspace_bytes(ctypes.byref(desc), T))
+
+
+def ftm_lora_linear(desc: LoraDesc, x, T, w, lora_a, lora_b, scale, adapter_ids, y, workspace, ws_bytes, stream=None,
+                    ldx: Optional[int] = None, ldy: Optional[int] = None):
+    """ldx / ldy: elements between rows of x / y (default: d_in / d_out, dense rows)."""
+    _check(library().ftm_lora_linear(ctypes.byref(desc), _ptr(x), desc.d_in if ldx is None else ldx, T, _ptr(w),
+                                     _ptr(lora_a), _ptr(lora_b), _ptr(scale), _ptr(adapter_ids), _ptr(y),
+                                     desc.d_out if ldy is None else ldy, _ptr(workspace), ws_bytes,
+                                     _stream(stream)))

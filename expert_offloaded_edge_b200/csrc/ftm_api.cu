@@ -44,6 +44,12 @@ const char* launch_expert_ffn_fp8(const FfnArgs& a, size_t s_gu_off, size_t s_d_
                                   cudaError_t* cerr);
 const char* launch_expert_ffn_mxfp4(const FfnArgs& a, size_t s_gu_off, size_t s_d_off, uint8_t* ws, cudaStream_t st,
                                     cudaError_t* cerr);
+const char* launch_gated_ffn(int act, const void* x, int T, int d, int I, const void* bank, size_t w_d_off, void* pre,
+                             void* h, void* y, cudaStream_t st, cudaError_t* cerr);
+const char* launch_gated_ffn_backward(int act, const void* x, int T, int d, int I, const void* bank, size_t w_d_off,
+                                      const void* pre, const void* dy, void* dx, void* dw_gu, void* dw_d, void* dgu,
+                                      void* h, cudaStream_t st, cudaError_t* cerr);
+const char* launch_lora(const LoraCall& c, cudaStream_t st, cudaError_t* cerr);
 }  // namespace ftm
 
 using namespace ftm;
@@ -410,6 +416,99 @@ ftm_status ffn_hits_then_misses(const ftm_layer_desc* L, const ftm_layer_weights
     g_prof[hooks[i]][1] = saved[i][1];
   }
   return s;
+}
+
+// ---- the dense projections (ftm_gated_ffn, ftm_lora_linear) ----
+
+constexpr int32_t kMaxDim = 1 << 20;      // d, I, d_in, d_out: tile counts stay far inside int32
+
+// A buffer of a call: rows of `cols` bytes, `pitch` bytes apart (one row: pitch = cols).
+struct Buf {
+  const char* name;
+  const void* p;
+  size_t rows, cols, pitch;
+  bool written;
+  size_t span() const { return rows ? (rows - 1) * pitch + cols : 0; }
+};
+
+// Whether two buffers share a byte.  Two column slices of one matrix (equal
+// pitch, disjoint columns) interleave without sharing any.
+bool share(const Buf& a, const Buf& b) {
+  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a.p), b0 = reinterpret_cast<uintptr_t>(b.p);
+  if (!a.span() || !b.span() || a0 + a.span() <= b0 || b0 + b.span() <= a0) return false;
+  if (a.pitch != b.pitch) return true;
+  const size_t off = (b0 >= a0 ? b0 - a0 : a.pitch - (a0 - b0) % a.pitch) % a.pitch;   // b's first column past a's
+  return !(off >= a.cols && off + b.cols <= a.pitch);
+}
+
+// Pointers of a call: set, 16-byte aligned, in memory of the current device,
+// and no written buffer shares a byte with another buffer.
+ftm_status check_bufs(const Buf* b, int n, const char* who) {
+  for (int i = 0; i < n; ++i) {
+    if (!b[i].p) return fail(FTM_ERR_INVALID_ARG, "%s: %s is NULL", who, b[i].name);
+    if (!aligned(b[i].p, 16)) return fail(FTM_ERR_INVALID_ARG, "%s: %s is not 16-byte aligned", who, b[i].name);
+  }
+  for (int i = 0; i < n; ++i)
+    for (int j = 0; j < n; ++j)
+      if (i != j && b[i].written && share(b[i], b[j]))
+        return fail(FTM_ERR_INVALID_ARG, "%s: %s overlaps %s", who, b[i].name, b[j].name);
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return cuda_fail(e, who);
+  }
+  for (int i = 0; i < n; ++i) {
+    cudaPointerAttributes pa;
+    if (cudaPointerGetAttributes(&pa, b[i].p) != cudaSuccess ||
+        (pa.type != cudaMemoryTypeDevice && pa.type != cudaMemoryTypeManaged) ||
+        (pa.type == cudaMemoryTypeDevice && pa.device != dev)) {
+      cudaGetLastError();
+      return fail(FTM_ERR_INVALID_ARG, "%s: %s is not memory of the current device (%d)", who, b[i].name, dev);
+    }
+  }
+  return FTM_OK;
+}
+
+// The result of a launcher (its message, or NULL) as a status.
+ftm_status launched(const char* msg, cudaError_t e, const char* who) {
+  if (!msg) return ok();
+  cudaGetLastError();          // reported here; not left for a later call to find
+  return e != cudaSuccess ? fail(FTM_ERR_CUDA, "%s: %s: %s", who, msg, cudaGetErrorString(e))
+                          : fail(FTM_ERR_CUDA, "%s: %s", who, msg);
+}
+
+ftm_status check_block(const ftm_layer_desc* L, int32_t act, int32_t T, const char* who) {
+  ftm_status s = check_desc(L);
+  if (s || (s = check_T(T))) return s;
+  if (L->wdtype != FTM_BF16) return fail(FTM_ERR_UNSUPPORTED, "%s: bf16 banks only (wdtype %d)", who, L->wdtype);
+  if (act != FTM_ACT_SILU && act != FTM_ACT_GELU_TANH) return fail(FTM_ERR_INVALID_ARG, "%s: unknown activation %d", who, act);
+  if (L->d > kMaxDim || L->I > kMaxDim)
+    return fail(FTM_ERR_UNSUPPORTED, "%s: d=%d, I=%d above %d", who, L->d, L->I, kMaxDim);
+  return FTM_OK;
+}
+
+size_t block_h_bytes(const ftm_layer_desc* L, int32_t T) { return al(static_cast<size_t>(T) * L->I * 2); }
+
+ftm_status check_lora(const ftm_lora_desc* D) {
+  static const char* who = "ftm_lora_linear";
+  if (!D) return fail(FTM_ERR_INVALID_ARG, "%s: descriptor is NULL", who);
+  if (D->reserved != 0) return fail(FTM_ERR_INVALID_ARG, "%s: reserved field must be 0", who);
+  if (D->wdtype < FTM_F32 || D->wdtype > FTM_MXFP4) return fail(FTM_ERR_INVALID_ARG, "%s: unknown wdtype %d", who, D->wdtype);
+  if (D->wdtype != FTM_BF16) return fail(FTM_ERR_UNSUPPORTED, "%s: bf16 only (wdtype %d)", who, D->wdtype);
+  if (D->d_in <= 0 || D->d_in % 8 || D->d_in > kMaxDim)
+    return fail(FTM_ERR_INVALID_ARG, "%s: d_in=%d must be a multiple of 8 in [8, %d]", who, D->d_in, kMaxDim);
+  if (D->d_out <= 0 || D->d_out % 8 || D->d_out > kMaxDim)
+    return fail(FTM_ERR_INVALID_ARG, "%s: d_out=%d must be a multiple of 8 in [8, %d]", who, D->d_out, kMaxDim);
+  if (D->rank < 8 || D->rank > 128 || D->rank % 8)
+    return fail(FTM_ERR_INVALID_ARG, "%s: rank=%d must be a multiple of 8 in [8, 128]", who, D->rank);
+  if (D->n_adapters < 1 || D->n_adapters > 65536)
+    return fail(FTM_ERR_INVALID_ARG, "%s: n_adapters=%d out of [1, 65536]", who, D->n_adapters);
+  return FTM_OK;
+}
+
+size_t lora_ws_bytes(const ftm_lora_desc* D, int32_t T) {
+  return al(static_cast<size_t>(T) * ((D->rank + 15) / 16 * 16) * 2);
 }
 
 thread_local char g_warn[256] = "";
@@ -967,6 +1066,129 @@ ftm_status ftm_moe_layer_forward_hybrid(const ftm_layer_desc* L, const ftm_layer
   H->last_host_rows = rows;
   H->last_host_ms = std::chrono::duration<double, std::milli>(t1 - t0).count();
   return ftm_combine(L, w.y, w.inv, w.gates, T, out, stream);
+}
+
+size_t ftm_gated_ffn_workspace_bytes(const ftm_layer_desc* L, int32_t T) {
+  if (check_block(L, FTM_ACT_SILU, T, "ftm_gated_ffn")) return 0;
+  return block_h_bytes(L, T);
+}
+
+ftm_status ftm_gated_ffn(const ftm_layer_desc* L, int32_t act, const void* x, int32_t T, const void* bank, void* pre,
+                         void* y, void* workspace, size_t ws_bytes, void* stream) {
+  static const char* who = "ftm_gated_ffn";
+  ftm_status s = check_block(L, act, T, who);
+  if (s) return s;
+  if (T == 0) return ok();
+  if ((s = check_ws(workspace, ws_bytes, block_h_bytes(L, T), who))) return s;
+  ftm_bank_layout bl;
+  bank_layout(L, &bl);
+  const size_t row = static_cast<size_t>(T) * L->d * 2, prow = static_cast<size_t>(T) * L->I * 4;
+  const size_t ws = block_h_bytes(L, T);
+  const Buf b[5] = {{"x", x, 1, row, row, false}, {"bank", bank, 1, bl.bank_bytes, bl.bank_bytes, false},
+                    {"y", y, 1, row, row, true}, {"workspace", workspace, 1, ws, ws, true},
+                    {"pre", pre, 1, prow, prow, true}};
+  if ((s = check_bufs(b, pre ? 5 : 4, who))) return s;
+  cudaError_t e = cudaSuccess;
+  const char* msg = launch_gated_ffn(act, x, T, L->d, L->I, bank, bl.w_d_off, pre, workspace, y, S_(stream), &e);
+  return launched(msg, e, who);
+}
+
+size_t ftm_gated_ffn_backward_workspace_bytes(const ftm_layer_desc* L, int32_t T) {
+  if (check_block(L, FTM_ACT_SILU, T, "ftm_gated_ffn_backward")) return 0;
+  return al(static_cast<size_t>(T) * L->I * 4) + block_h_bytes(L, T);
+}
+
+ftm_status ftm_gated_ffn_backward(const ftm_layer_desc* L, int32_t act, const void* x, int32_t T, const void* bank,
+                                  const void* pre, const void* dy, void* dx, void* dbank, void* workspace,
+                                  size_t ws_bytes, void* stream) {
+  static const char* who = "ftm_gated_ffn_backward";
+  ftm_status s = check_block(L, act, T, who);
+  if (s) return s;
+  if (!dx && !dbank) return fail(FTM_ERR_INVALID_ARG, "%s: dx and dbank are both NULL", who);
+  ftm_bank_layout bl;
+  bank_layout(L, &bl);
+  cudaError_t e = cudaSuccess;
+  uint8_t* db = static_cast<uint8_t*>(dbank);
+  if (T == 0) {
+    if (!dbank) return ok();
+    const Buf b[1] = {{"dbank", dbank, 1, bl.bank_bytes, bl.bank_bytes, true}};
+    if ((s = check_bufs(b, 1, who))) return s;
+    e = cudaMemsetAsync(db, 0, bl.w_d_off + bl.w_d_bytes, S_(stream));
+    return launched(e == cudaSuccess ? nullptr : "clearing the gradients failed", e, who);
+  }
+  const size_t dgu_bytes = al(static_cast<size_t>(T) * L->I * 4);
+  const size_t ws = dgu_bytes + block_h_bytes(L, T);
+  if ((s = check_ws(workspace, ws_bytes, ws, who))) return s;
+  const size_t row = static_cast<size_t>(T) * L->d * 2, prow = static_cast<size_t>(T) * L->I * 4;
+  Buf b[7] = {{"x", x, 1, row, row, false}, {"bank", bank, 1, bl.bank_bytes, bl.bank_bytes, false},
+              {"pre", pre, 1, prow, prow, false}, {"dy", dy, 1, row, row, false},
+              {"workspace", workspace, 1, ws, ws, true}};
+  int n = 5;
+  if (dx) b[n++] = {"dx", dx, 1, row, row, true};
+  if (dbank) b[n++] = {"dbank", dbank, 1, bl.bank_bytes, bl.bank_bytes, true};
+  if ((s = check_bufs(b, n, who))) return s;
+  uint8_t* w = static_cast<uint8_t*>(workspace);
+  const char* msg = launch_gated_ffn_backward(act, x, T, L->d, L->I, bank, bl.w_d_off, pre, dy, dx,
+                                              dbank ? db + bl.w_gu_off : nullptr, dbank ? db + bl.w_d_off : nullptr, w,
+                                              w + dgu_bytes, S_(stream), &e);
+  return launched(msg, e, who);
+}
+
+size_t ftm_lora_workspace_bytes(const ftm_lora_desc* D, int32_t T) {
+  if (check_lora(D) || check_T(T)) return 0;
+  return lora_ws_bytes(D, T);
+}
+
+ftm_status ftm_lora_linear(const ftm_lora_desc* D, const void* x, int64_t ldx, int32_t T, const void* w,
+                           const void* lora_a, const void* lora_b, const float* scale, const int32_t* adapter_ids,
+                           void* y, int64_t ldy, void* workspace, size_t ws_bytes, void* stream) {
+  static const char* who = "ftm_lora_linear";
+  ftm_status s = check_lora(D);
+  if (s || (s = check_T(T))) return s;
+  if (ldx < D->d_in || ldx % 8 || ldx > (1ll << 32))
+    return fail(FTM_ERR_INVALID_ARG, "%s: ldx=%lld must be a multiple of 8 >= d_in=%d", who, static_cast<long long>(ldx), D->d_in);
+  if (ldy < D->d_out || ldy % 8 || ldy > (1ll << 32))
+    return fail(FTM_ERR_INVALID_ARG, "%s: ldy=%lld must be a multiple of 8 >= d_out=%d", who, static_cast<long long>(ldy), D->d_out);
+  if (T == 0) return ok();
+  const size_t ws = lora_ws_bytes(D, T);
+  if ((s = check_ws(workspace, ws_bytes, ws, who))) return s;
+  const size_t n = D->n_adapters, di = D->d_in, dn = D->d_out, r = D->rank, t = T;
+  Buf b[8] = {{"x", x, t, di * 2, static_cast<size_t>(ldx) * 2, false}, {"w", w, 1, dn * di * 2, dn * di * 2, false},
+              {"lora_a", lora_a, 1, n * r * di * 2, n * r * di * 2, false},
+              {"lora_b", lora_b, 1, n * dn * r * 2, n * dn * r * 2, false},
+              {"y", y, t, dn * 2, static_cast<size_t>(ldy) * 2, true}, {"workspace", workspace, 1, ws, ws, true},
+              {nullptr}, {nullptr}};
+  int m = 6;
+  // 4-byte values may start anywhere a 4-byte value may
+  struct { const char* name; const void* p; size_t bytes; bool need; } f[2] = {
+      {"adapter_ids", adapter_ids, t * 4, true}, {"scale", scale, n * 4, false}};
+  for (auto& v : f) {
+    if (!v.p && v.need) return fail(FTM_ERR_INVALID_ARG, "%s: %s is NULL", who, v.name);
+    if (!v.p) continue;
+    if (!aligned(v.p, 4)) return fail(FTM_ERR_INVALID_ARG, "%s: %s is not 4-byte aligned", who, v.name);
+    const uintptr_t lo = reinterpret_cast<uintptr_t>(v.p) & ~uintptr_t{15};
+    b[m++] = {v.name, reinterpret_cast<const void*>(lo), 1, v.bytes, v.bytes, false};
+  }
+  if ((s = check_bufs(b, m, who))) return s;
+  LoraCall c;
+  c.T = T;
+  c.d_in = D->d_in;
+  c.d_out = D->d_out;
+  c.n = D->n_adapters;
+  c.rank = D->rank;
+  c.x = static_cast<const uint16_t*>(x);
+  c.w = static_cast<const uint16_t*>(w);
+  c.a = static_cast<const uint16_t*>(lora_a);
+  c.b = static_cast<const uint16_t*>(lora_b);
+  c.ldx = ldx;
+  c.ldy = ldy;
+  c.scale = scale;
+  c.ids = adapter_ids;
+  c.y = static_cast<uint16_t*>(y);
+  c.v = static_cast<uint16_t*>(workspace);
+  cudaError_t e = cudaSuccess;
+  const char* msg = launch_lora(c, S_(stream), &e);
+  return launched(msg, e, who);
 }
 
 }  // extern "C"

@@ -244,4 +244,15 @@ struct FfnArgs {
   uint8_t* h;    // workspace [rows][I]
 };
 
+// Arguments of the adapter projection's launcher.
+struct LoraCall {
+  int T, d_in, d_out, n, rank;
+  const uint16_t *x, *w, *a, *b;
+  int64_t ldx, ldy;
+  const float* scale;
+  const int32_t* ids;
+  uint16_t* y;
+  uint16_t* v;        // workspace [T][rank rounded up to 16]
+};
+
 }  // namespace ftm

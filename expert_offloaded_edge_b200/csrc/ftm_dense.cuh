@@ -1,0 +1,544 @@
+// The dense (ungrouped) bf16 GEMM engine on CTA pairs: D = A B^T over tiles of
+// 256 rows x BN columns, one tile per pair of CTAs (tcgen05 cta_group::2).
+//
+// Rows (tokens, or the rows of a weight gradient) are on the MMA's M side, so
+// that a thread of the epilogue owns one row and consecutive columns: the
+// gate/up pairing, the activation's gradient and the stores need no exchange
+// between threads.  Either operand may be stored with its depth innermost
+// (K-major: activations and weights of a forward product) or with its rows
+// innermost (MN-major: what a transposed product reads), which is a choice of
+// tensor-map box and matrix descriptor, never a transposing copy:
+//   K-major  stage tile: [rows][64 deep], one box {64 deep, rows}
+//   MN-major stage tile: boxes {64 rows, 64 deep}, 8 KB each, one per 64 rows
+// A launch takes up to three products ("problems"), so the independent
+// products of a backward pass fill the GPU together.
+//
+// Roles: warp 0 issues the TMA loads, warp 1 of the even CTA the MMAs, warps
+// 2-5 drain the accumulators (double-buffered in TMEM: BN = 256 uses all 512
+// columns) through swizzled staging rows and TMA stores, which clip the ragged
+// rows and columns.  With LORA, warps 6-9 feed the adapters' K range (see
+// ftm_lora.cuh).  No TMA multicast.
+#pragma once
+
+#include "ftm_gemm.cuh"
+#include "ftm_lora.cuh"
+
+namespace ftm {
+
+constexpr int kDTileM = 256;                   // rows per tile (128 per CTA)
+constexpr int kDBK = 64;                       // depth per stage
+constexpr uint32_t kDABytes = 128 * 128;       // 128 rows x 64 deep of bf16 per CTA
+constexpr int kDSlotBytes = 32 * 128;          // one warp's staging slot: 32 rows x 64 columns of bf16
+constexpr int kDProblems = 3;
+
+enum DenseEpi {
+  kEpiStore = 0,   // c0 = D
+  kEpiGated = 1,   // D holds gate and up columns: c0 = act(g) * u; c1 = g, c2 = u when kept
+  kEpiDgate = 2    // D = dh: c0 = dg, c1 = du, c2 = h, from the kept g and u
+};
+
+struct DenseProblem {
+  CUtensorMap a, b, c0, c1, c2;
+  int M, N;          // rows, output columns (gated: columns of h)
+  int nt;            // column tiles
+  int kb;            // 64-deep blocks
+  int tiles;
+  int a_mn, b_mn;    // operand stored rows-innermost
+  int up_row0;       // gated: row of B where the up projection starts
+};
+
+struct DenseArgs {
+  DenseProblem p[kDProblems];
+  int n;             // problems, deepest first
+  int act;           // ftm_act
+  int keep;          // gated: store g and u; dgate: store h
+  const uint16_t* pre;   // dgate: kept g and u, [M][2N]
+  // tile schedule (see dense_tile_at)
+  int n_long, n_short, short_extra;
+  LoraArgs lora;
+};
+
+// ---- descriptors ---------------------------------------------------------------
+// MN-major operand, 128-byte swizzle: atoms of 64 rows (128 bytes) x 8 deep, the
+// next 8 deep 1024 bytes on, the next 64 rows one box (8 KB) on.
+__device__ __forceinline__ uint64_t smem_desc_mn_sw128(uint32_t saddr) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((saddr >> 4) & 0x3FFFu);
+  d |= static_cast<uint64_t>(8192u >> 4) << 16;
+  d |= static_cast<uint64_t>(1024u >> 4) << 32;
+  d |= static_cast<uint64_t>(1u) << 46;
+  d |= static_cast<uint64_t>(2u) << 61;
+  return d;
+}
+
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* m, const void* src, int32_t c0, int32_t c1) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
+                   reinterpret_cast<uint64_t>(m)),
+               "r"(smem_u32(src)), "r"(c0), "r"(c1)
+               : "memory");
+}
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void bulk_wait_read() {
+  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// One row's 32 columns into half (0: columns 0-31, 1: 32-63) of a staging slot
+// in the layout the 128-byte-swizzled store map reads.
+__device__ __forceinline__ void stage_half(uint8_t* slot, int row, int half, const uint32_t* w) {
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    const int chunk = (half * 4 + c) ^ (row & 7);
+    *reinterpret_cast<uint4*>(slot + row * 128 + chunk * 16) = make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+  }
+}
+
+// ---- tile schedule ---------------------------------------------------------------
+// The pair's i-th tile, or -1.  Tiles [0, n_long) have the deepest K and go
+// round the pairs first; a pair that got one fewer takes short_extra shallow
+// tiles in its place, and the rest go round from the last pair down.  All from
+// sizes: the assignment never depends on timing.
+__device__ __forceinline__ int dense_tile_at(const DenseArgs& g, int pair, int np, int i) {
+  const int rem = g.n_long % np;
+  const int mine = g.n_long / np + (pair < rem ? 1 : 0);
+  if (i < mine) return pair + i * np;
+  i -= mine;
+  const int room = np - rem;
+  const int s1 = rem ? min(g.n_short, g.short_extra * room) : 0;
+  if (pair >= rem && s1) {
+    const int first = pair - rem;
+    const int have = first < s1 ? (s1 - first - 1) / room + 1 : 0;
+    if (i < have) return g.n_long + first + i * room;
+    i -= have;
+  }
+  const int s = s1 + (np - 1 - pair) + i * np;
+  return s < g.n_short ? g.n_long + s : -1;
+}
+
+struct DenseTile {
+  int p, m, n;
+};
+
+// Tiles of a problem run down bands of 8 row tiles, so that the tiles in
+// flight share both operands' blocks in L2.
+__device__ __forceinline__ DenseTile dense_decode(const DenseArgs& g, int t) {
+  int p = 0;
+  while (p + 1 < g.n && t >= g.p[p].tiles) { t -= g.p[p].tiles; ++p; }
+  const int nt = g.p[p].nt, mt = g.p[p].tiles / nt;
+  const int band = t / (8 * nt);
+  const int rows = min(8, mt - band * 8);
+  const int in = t - band * 8 * nt;
+  DenseTile d;
+  d.p = p;
+  d.m = band * 8 + in % rows;
+  d.n = in / rows;
+  return d;
+}
+
+template <int BN, bool LORA>
+struct DenseShape {
+  static constexpr uint32_t kBBytes = BN / 2 * 128;
+  static constexpr uint32_t kStage = kDABytes + kBBytes;
+  static constexpr int kSlots = LORA ? 2 : 3;                      // staging slots per epilogue warp
+  static constexpr uint32_t kStaging = 4 * kSlots * kDSlotBytes;
+  static constexpr uint32_t kExt = LORA ? kLoraRing * (128 * 32 + BN / 2 * 32) : 0;
+  static constexpr int kStages = BN == 256 ? 5 : 6;
+  static constexpr size_t kSmem = 1024 + static_cast<size_t>(kStages) * kStage + kStaging + kExt;
+  static constexpr int kThreads = LORA ? 320 : 192;
+};
+
+template <int EPI, int BN, bool LORA>
+__global__ void __launch_bounds__(DenseShape<BN, LORA>::kThreads, 1)
+    dense_kernel(const __grid_constant__ DenseArgs g) {
+  using S = DenseShape<BN, LORA>;
+  constexpr int kStages = S::kStages;
+  constexpr uint32_t kTmemCols = 2 * BN;
+  constexpr int kOutCols = EPI == kEpiGated ? BN / 2 : BN;   // output columns per tile
+
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t full_bar[kStages], empty_bar[kStages], tfull_bar[2], tempty_bar[2];
+  __shared__ uint32_t tmem_holder;
+  __shared__ LoraShared<LORA> ls;
+
+  const uint32_t smem_base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  uint8_t* smem = smem_raw + (smem_base - smem_u32(smem_raw));
+  uint8_t* staging = smem + static_cast<size_t>(kStages) * S::kStage;
+  uint8_t* ext = staging + S::kStaging;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const uint32_t rank = cluster_rank();
+  const bool leader = rank == 0;
+  const int np = gridDim.x / 2, pair = blockIdx.x / 2;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) { mbar_init(&full_bar[s], 1); mbar_init(&empty_bar[s], 1); }
+    for (int a = 0; a < 2; ++a) { mbar_init(&tfull_bar[a], LORA ? 2 : 1); mbar_init(&tempty_bar[a], 8); }
+    if constexpr (LORA) ls.init();
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_holder)),
+                 "r"(kTmemCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  if (warp == 0 && lane == 0) {
+    for (int p = 0; p < g.n; ++p) { tma_prefetch_desc(&g.p[p].a); tma_prefetch_desc(&g.p[p].b); }
+  }
+  pdl_wait();
+  pdl_trigger();
+  tc_fence_before();
+  cluster_sync_all();     // barriers initialised and TMEM allocated in both CTAs
+  tc_fence_after();
+  const uint32_t tmem_base = tmem_holder;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int i = 0, t; ok && (t = dense_tile_at(g, pair, np, i)) >= 0; ++i) {
+        const DenseTile ti = dense_decode(g, t);
+        const DenseProblem& P = g.p[ti.p];
+        const int ar = ti.m * kDTileM + static_cast<int>(rank) * 128;
+        // gated: the even CTA stages gate rows, the odd CTA the matching up rows
+        const int br = EPI == kEpiGated ? ti.n * kOutCols + (leader ? 0 : P.up_row0)
+                                        : ti.n * BN + static_cast<int>(rank) * (BN / 2);
+        for (int kb = 0; kb < P.kb; ++kb) {
+          if (!mbar_wait_cl(&empty_bar[stage], phase ^ 1u)) { ok = false; break; }
+          if (leader) mbar_arrive_expect_tx(&full_bar[stage], 2 * S::kStage);
+          const uint32_t lbar = mapa_rank(smem_u32(&full_bar[stage]), 0);
+          uint8_t* sa = smem + static_cast<size_t>(stage) * S::kStage;
+          uint8_t* sb = sa + kDABytes;
+          const int kc = kb * kDBK;
+          if (P.a_mn) {
+            tma2_load_2d(sa, &P.a, lbar, ar, kc);
+            tma2_load_2d(sa + 8192, &P.a, lbar, ar + 64, kc);
+          } else {
+            tma2_load_2d(sa, &P.a, lbar, kc, ar);
+          }
+          if (P.b_mn) {
+#pragma unroll
+            for (int j = 0; j < BN / 128; ++j) tma2_load_2d(sb + j * 8192, &P.b, lbar, br + j * 64, kc);
+          } else {
+            tma2_load_2d(sb, &P.b, lbar, kc, br);
+          }
+          if (++stage == kStages) { stage = 0; phase ^= 1u; }
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (leader && lane == 0) {
+      int stage = 0, es = 0;
+      uint32_t phase = 0, ephase = 0;
+      bool ok = true;
+      for (int i = 0, t; ok && (t = dense_tile_at(g, pair, np, i)) >= 0; ++i) {
+        const DenseTile ti = dense_decode(g, t);
+        const DenseProblem& P = g.p[ti.p];
+        const int ab = i & 1;
+        if (!mbar_wait_cl(&tempty_bar[ab], ((i >> 1) & 1) ^ 1u)) break;
+        tc_fence_after();
+        const uint32_t d = tmem_base + ab * BN;
+        const bool amn = P.a_mn, bmn = P.b_mn;
+        const uint32_t idesc = idesc_bf16_f32(256, BN) | (amn ? 1u << 15 : 0u) | (bmn ? 1u << 16 : 0u);
+        // a 16-deep step: 32 bytes along a K-major row, 16 rows of 128 bytes of an MN-major box
+        const uint32_t astep = amn ? 2048 : 32, bstep = bmn ? 2048 : 32;
+        for (int kb = 0; kb < P.kb; ++kb) {
+          if (!mbar_wait_cl(&full_bar[stage], phase)) { ok = false; break; }
+          tc_fence_after();
+          const uint32_t sa = smem_u32(smem + static_cast<size_t>(stage) * S::kStage);
+          const uint32_t sb = sa + kDABytes;
+#pragma unroll
+          for (int kk = 0; kk < kDBK / 16; ++kk) {
+            const uint64_t da = amn ? smem_desc_mn_sw128(sa + kk * astep) : smem_desc_sw128(sa + kk * astep);
+            const uint64_t db = bmn ? smem_desc_mn_sw128(sb + kk * bstep) : smem_desc_sw128(sb + kk * bstep);
+            umma2_f16(d, da, db, idesc, (kb | kk) != 0 ? 1u : 0u);
+          }
+          umma2_commit_both(&empty_bar[stage]);
+          if (++stage == kStages) { stage = 0; phase ^= 1u; }
+        }
+        if constexpr (LORA) {
+          // the adapters' K range: one 16-deep slice per message until the tile's last
+          uint32_t poison = 0;
+          bool last = false;
+          while (ok && !last) {
+            if (!mbar_wait_cl(&ls.full[es], ephase)) { ok = false; break; }
+            tc_fence_after();
+            const uint32_t msg = ls.msg[es];
+            last = (msg & kLoraLast) != 0;
+            if (msg & kLoraData) {
+              poison |= (msg | ls.msg_peer[es]) & kLoraPoison;
+              const uint32_t sv = smem_u32(ext + es * (128 * 32 + BN / 2 * 32));
+              umma2_f16(d, smem_desc_k32(sv), smem_desc_k32(sv + 128 * 32), idesc_bf16_f32(256, BN), 1u);
+            }
+            umma2_commit_both(&ls.empty[es]);
+            if (++es == kLoraRing) { es = 0; ephase ^= 1u; }
+          }
+          if (ok) {
+            // the epilogue of both CTAs learns whether a slice held non-finite weights
+            const uint32_t peer = mapa_rank(smem_u32(&ls.poison[ab]), 1);
+            ls.poison[ab] = poison;
+            asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(peer), "r"(poison) : "memory");
+            mbar_arrive(&tfull_bar[ab]);
+            mbar_arrive_remote(mapa_rank(smem_u32(&tfull_bar[ab]), 1));
+          }
+        }
+        if (ok) umma2_commit_both(&tfull_bar[ab]);
+      }
+    }
+    __syncwarp();
+  } else if (warp < 6) {
+    const int q = warp % 4;           // TMEM lane quadrant
+    const uint32_t tempty0 = mapa_rank(smem_u32(&tempty_bar[0]), 0);
+    const uint32_t tempty1 = mapa_rank(smem_u32(&tempty_bar[1]), 0);
+    uint8_t* slots = staging + (warp - 2) * S::kSlots * kDSlotBytes;
+    int chunk = 0;                    // chunks stored so far: kEpiStore alternates between two slots
+    for (int i = 0, t; (t = dense_tile_at(g, pair, np, i)) >= 0; ++i) {
+      const DenseTile ti = dense_decode(g, t);
+      const DenseProblem& P = g.p[ti.p];
+      const int ab = i & 1;
+      if (!__all_sync(0xffffffffu, mbar_wait_cl(&tfull_bar[ab], (i >> 1) & 1))) break;
+      tc_fence_after();
+      const int row0 = ti.m * kDTileM + static_cast<int>(rank) * 128 + q * 32;   // this warp's 32 rows
+      const int row = row0 + lane;
+      const int col0 = ti.n * kOutCols;
+      const uint32_t tb = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + ab * BN;
+      bool poison = false;
+      if constexpr (LORA) poison = ls.poison[ab] != 0;
+      if (row0 < P.M) {
+#pragma unroll 1
+        for (int c0 = 0; c0 < kOutCols && col0 + c0 < P.N; c0 += 64) {
+          const int cols = P.N - col0 - c0;      // columns left, of which this chunk takes 64
+          uint8_t* s0 = slots;
+          if (EPI == kEpiStore) {
+            s0 = slots + (chunk++ & 1) * kDSlotBytes;
+            if (lane == 0) bulk_wait_read<1>();  // the store before last has read its slot
+          } else {
+            if (lane == 0) bulk_wait_read<0>();
+          }
+          __syncwarp();
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf) {
+            const int c = c0 + hf * 32;
+            float v[32];
+            tmem_ld16(tb + c, v);
+            tmem_ld16(tb + c + 16, v + 16);
+            if constexpr (EPI == kEpiStore) {
+              tmem_ld_wait();
+              if constexpr (LORA) {
+                if (poison && row < P.M) {
+#pragma unroll
+                  for (int j = 0; j < 32; ++j)
+                    if (hf * 32 + j < cols) v[j] += lora_nonfinite_term(g.lora, row, col0 + c + j);
+                }
+              }
+              uint32_t w[16];
+#pragma unroll
+              for (int j = 0; j < 16; ++j) w[j] = pack_bf16(v[2 * j], v[2 * j + 1]);
+              stage_half(s0, lane, hf, w);
+            } else if constexpr (EPI == kEpiGated) {
+              float u[32];
+              tmem_ld16(tb + BN / 2 + c, u);
+              tmem_ld16(tb + BN / 2 + c + 16, u + 16);
+              tmem_ld_wait();
+              uint32_t w[16];
+              if (g.keep) {
+#pragma unroll
+                for (int j = 0; j < 16; ++j) w[j] = pack_bf16(v[2 * j], v[2 * j + 1]);
+                stage_half(slots + kDSlotBytes, lane, hf, w);
+#pragma unroll
+                for (int j = 0; j < 16; ++j) w[j] = pack_bf16(u[2 * j], u[2 * j + 1]);
+                stage_half(slots + 2 * kDSlotBytes, lane, hf, w);
+              }
+#pragma unroll
+              for (int j = 0; j < 16; ++j)
+                w[j] = pack_bf16(act_value(v[2 * j], g.act) * u[2 * j], act_value(v[2 * j + 1], g.act) * u[2 * j + 1]);
+              stage_half(s0, lane, hf, w);
+            } else {
+              // g and u of this row: 32 columns are 64 bytes of each (N is a multiple of 128)
+              uint4 gv[4], uv[4];
+              const uint16_t* pg = g.pre + static_cast<size_t>(row) * (2 * static_cast<size_t>(P.N)) + col0 + c;
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                gv[k] = row < P.M ? __ldg(reinterpret_cast<const uint4*>(pg) + k) : make_uint4(0, 0, 0, 0);
+                uv[k] = row < P.M ? __ldg(reinterpret_cast<const uint4*>(pg + P.N) + k) : make_uint4(0, 0, 0, 0);
+              }
+              tmem_ld_wait();
+              const uint32_t* gw = reinterpret_cast<const uint32_t*>(gv);
+              const uint32_t* uw = reinterpret_cast<const uint32_t*>(uv);
+              uint32_t wg[16], wu[16], wh[16];
+#pragma unroll
+              for (int j = 0; j < 16; ++j) {
+                float dg[2], du[2], h[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                  const float z = __uint_as_float(e ? gw[j] & 0xffff0000u : gw[j] << 16);
+                  const float u = __uint_as_float(e ? uw[j] & 0xffff0000u : uw[j] << 16);
+                  const float dh = v[2 * j + e];
+                  float s, zq;
+                  act_parts(z, g.act, s, zq);
+                  const float a = z * s;
+                  dg[e] = dh * u * fmaf(zq * s, 1.f - s, s);
+                  du[e] = dh * a;
+                  h[e] = a * u;
+                }
+                wg[j] = pack_bf16(dg[0], dg[1]);
+                wu[j] = pack_bf16(du[0], du[1]);
+                wh[j] = pack_bf16(h[0], h[1]);
+              }
+              stage_half(slots, lane, hf, wg);
+              stage_half(slots + kDSlotBytes, lane, hf, wu);
+              if (g.keep) stage_half(slots + 2 * kDSlotBytes, lane, hf, wh);
+            }
+          }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+          if (lane == 0) {
+            tma_store_2d(&P.c0, s0, col0 + c0, row0);
+            if (EPI == kEpiDgate || (EPI == kEpiGated && g.keep)) tma_store_2d(&P.c1, slots + kDSlotBytes, col0 + c0, row0);
+            if (EPI != kEpiStore && g.keep) tma_store_2d(&P.c2, slots + 2 * kDSlotBytes, col0 + c0, row0);
+            bulk_commit();
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if (leader) mbar_arrive(&tempty_bar[ab]);
+        else mbar_arrive_remote(ab ? tempty1 : tempty0);
+      }
+    }
+    if (lane == 0) bulk_wait_all();
+    __syncwarp();
+  } else {
+    if constexpr (LORA) {
+      // one row of the tile per thread; both CTAs list the adapters of all 256 rows and feed the same slices,
+      // each its own 128 rows of v and its own half of the output columns
+      LoraRing ring;
+      const LoraArgs& L = g.lora;
+      const int e = threadIdx.x - 192;
+      bool ok = true;
+      for (int i = 0, t; ok && (t = dense_tile_at(g, pair, np, i)) >= 0; ++i) {
+        const DenseTile ti = dense_decode(g, t);
+        const int m0 = ti.m * kDTileM;
+        const int i0 = lora_id(L.ids, L.T, L.n, m0 + e), i1 = lora_id(L.ids, L.T, L.n, m0 + 128 + e);
+        const int nl = lora_list<256>(ls, e, i0, i1);
+        auto send = [&](uint32_t slot, bool last, bool bad) {
+          if (leader) {
+            ls.msg[slot] = kLoraData | (last ? kLoraLast : 0u) | (bad ? kLoraPoison : 0u);
+            mbar_arrive(&ls.full[slot]);
+          } else {
+            asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(mapa_rank(smem_u32(&ls.msg_peer[slot]), 0)),
+                         "r"(bad ? kLoraPoison : 0u)
+                         : "memory");
+            mbar_arrive_remote(mapa_rank(smem_u32(&ls.full[slot]), 0));
+          }
+        };
+        if (nl == 0) {
+          // no adapter in the tile: one message without data
+          const uint32_t slot = ring.count % kLoraRing;
+          ok = mbar_wait_cl(&ls.empty[slot], ((ring.count / kLoraRing) & 1u) ^ 1u);
+          ok = feed_all(ok);
+          if (ok && e == 0) {
+            mbar_arrive(&ls.landed[slot]);      // every use of a slot is one phase of its barriers
+            if (leader) {
+              ls.msg[slot] = kLoraLast;
+              mbar_arrive(&ls.full[slot]);
+            } else {
+              mbar_arrive_remote(mapa_rank(smem_u32(&ls.full[slot]), 0));
+            }
+          }
+          ring.count += 1;
+          continue;
+        }
+        ok = lora_feed<128, BN / 2>(L, ls, ring, ext, 0, 128 * 32, 128 * 32 + BN / 2 * 32, e, nl, 0, 1,
+                                    m0 + static_cast<int>(rank) * 128 + e, leader ? i0 : i1,
+                                    ti.n * BN + static_cast<int>(rank) * (BN / 2), send);
+      }
+    }
+  }
+  tc_fence_before();
+  cluster_sync_all();     // no CTA leaves while its pair may still signal it
+  tc_fence_after();
+  if (warp == 1)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(kTmemCols) : "memory");
+}
+
+// ---- host ------------------------------------------------------------------------
+
+// Operand map: K-major dims {K, rows}, box {64, box_rows}; MN-major dims {rows, K}, box {64, 64}.
+inline bool dense_operand_map(CUtensorMap* m, const void* base, bool mn, uint64_t rows, uint64_t K, uint64_t pitch_bytes,
+                              uint32_t box_rows) {
+  return make_map_sw128(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, mn ? rows : K, mn ? K : rows, pitch_bytes, 0, 0,
+                        mn ? 64 : box_rows);
+}
+
+// Store map: dims {cols, rows}, box {64 columns, 32 rows}; clips what lies outside.
+inline bool dense_store_map(CUtensorMap* m, void* base, uint64_t cols, uint64_t rows, uint64_t pitch_bytes) {
+  return make_map_sw128(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, cols, rows, pitch_bytes, 0, 0, 32);
+}
+
+inline void dense_tiles(DenseProblem& P, int M, int N, int K, int out_cols) {
+  P.M = M;
+  P.N = N;
+  P.kb = (K + kDBK - 1) / kDBK;
+  P.nt = (N + out_cols - 1) / out_cols;
+  P.tiles = (M + kDTileM - 1) / kDTileM * P.nt;
+}
+
+// Orders the problems by depth and sets the schedule.
+inline void dense_schedule(DenseArgs& a) {
+  for (int i = 1; i < a.n; ++i)
+    for (int j = i; j > 0 && a.p[j].kb > a.p[j - 1].kb; --j) { DenseProblem t = a.p[j]; a.p[j] = a.p[j - 1]; a.p[j - 1] = t; }
+  a.n_long = a.n_short = 0;
+  int kshort = 1;
+  for (int i = 0; i < a.n; ++i) {
+    if (a.p[i].kb == a.p[0].kb) a.n_long += a.p[i].tiles;
+    else { a.n_short += a.p[i].tiles; kshort = kshort > a.p[i].kb ? kshort : a.p[i].kb; }
+  }
+  a.short_extra = (a.p[0].kb + kshort / 2) / kshort;
+}
+
+template <int EPI, int BN, bool LORA>
+cudaError_t launch_dense(DenseArgs& a, cudaStream_t st) {
+  using S = DenseShape<BN, LORA>;
+  dense_schedule(a);
+  auto kern = dense_kernel<EPI, BN, LORA>;
+  cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(S::kSmem));
+  if (err != cudaSuccess) return err;
+  cudaLaunchConfig_t cfg = {};
+  cfg.blockDim = dim3(S::kThreads);
+  cfg.dynamicSmemBytes = S::kSmem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  // one wave of pairs: as many as the GPCs can hold at once
+  static const int pairs_max = [&] {
+    cfg.gridDim = dim3(num_sms() / 2 * 2);
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n <= 0) {
+      (void)cudaGetLastError();
+      n = num_sms() / 2;
+    }
+    return n < num_sms() / 2 ? n : num_sms() / 2;
+  }();
+  const int tiles = a.n_long + a.n_short;
+  cfg.gridDim = dim3(2 * (tiles < pairs_max ? tiles : pairs_max));
+  cfg.numAttrs = 2;
+  return count_launch(cudaLaunchKernelEx(&cfg, kern, a));
+}
+
+}  // namespace ftm

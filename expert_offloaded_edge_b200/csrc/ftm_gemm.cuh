@@ -16,6 +16,30 @@ constexpr uint32_t kATileBytes = 128 * 128;   // one 128-row x 128-byte weight t
 // denominator overflows to +inf and the quotient is -0.
 __device__ __forceinline__ float silu(float z) { return __fdividef(z, 1.f + __expf(-z)); }
 
+// ---- activation --------------------------------------------------------------
+// act(z) = z s with s = sigmoid(q(z)); act'(z) = s + z s (1 - s) q'(z).
+//   SiLU: q = z.   GELU (tanh form): (1 + tanh(w)) / 2 = sigmoid(2 w), so
+//   q = 2 sqrt(2/pi) (z + 0.044715 z^3).
+// The GELU argument is clamped to [-12, 12], where s is 0 or 1 to fp32, so the
+// cube cannot overflow into 0 * inf.
+__device__ __forceinline__ void act_parts(float z, int act, float& s, float& zq) {
+  float q = z;
+  zq = z;
+  if (act == FTM_ACT_GELU_TANH) {
+    const float c = fminf(fmaxf(z, -12.f), 12.f);
+    const float c2 = c * c;
+    q = 1.5957691216057308f * c * fmaf(0.044715f, c2, 1.f);
+    zq = 1.5957691216057308f * c * fmaf(0.134145f, c2, 1.f);
+  }
+  s = __fdividef(1.f, 1.f + __expf(-q));
+}
+
+__device__ __forceinline__ float act_value(float z, int act) {
+  float s, zq;
+  act_parts(z, act, s, zq);
+  return z * s;
+}
+
 // ---- thread-block cluster helpers ------------------------------------------
 __device__ __forceinline__ uint32_t cluster_nranks() {
   uint32_t r;
@@ -108,6 +132,17 @@ __device__ __forceinline__ void umma2_commit_both(uint64_t* bar) {
       "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
           smem_u32(bar)),
       "h"(mask)
+      : "memory");
+}
+
+// D[tmem of both CTAs] (+)= A * B^T on the pair's staged operands, kind::f16.
+__device__ __forceinline__ void umma2_f16(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                          uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
 

@@ -1,0 +1,224 @@
+// Low-rank adapters of many requests beside a shared projection (device parts).
+//
+//   y[t] = x[t] W^T + s[a] (x[t] A[a]^T) B[a]^T,   a = adapter id of token t
+//
+// The projection kernels run over K = d_in and then over an extra K range: for
+// every adapter that occurs in the token tile, the products v B[a]^T with
+// v = s (x A[a]^T) of that adapter's tokens and zeros for all others, added in
+// the same accumulator.  So a tile may mix any requests, nothing is sorted, W
+// is read once, and B[a] is read by the tiles that hold one of its tokens.  The
+// extra range is fed in slices of 16 (one MMA deep): slices of v are written to
+// shared memory by threads, slices of B[a] come by TMA.
+//
+// A zero row does not mask an infinity or NaN of another request's adapter
+// (0 * inf = NaN).  The feeding threads see every slice of B[a], so they take
+// non-finite weights out of it and flag the tile; the epilogue of a flagged
+// tile adds the exact non-finite terms to the adapter's own tokens only.
+#pragma once
+
+#include "ftm_gemm.cuh"
+
+namespace ftm {
+
+constexpr int kLoraRing = 4;              // slices in flight
+constexpr uint32_t kLoraData = 1, kLoraLast = 2, kLoraPoison = 4;
+
+struct LoraArgs {
+  CUtensorMap b;             // B pool: dims {rank, d_out, adapters}, box {16, rows of a slice}, 32-byte swizzle
+  const int32_t* ids;        // [T] adapter of each token, -1: none
+  const uint16_t* v;         // [T][rp] bf16, s (x A^T); rows of tokens without an adapter are never read
+  const uint16_t* b_pool;    // [adapters][d_out][rank]
+  int T, n, rank, rp, d_out; // rp: rank rounded up to 16
+};
+
+// K-major operand slice, 16 deep: rows of 32 bytes, 32-byte swizzle (the two
+// 16-byte halves of a row change places where bit 2 of the row is set), 8 rows = 256 bytes.
+__device__ __forceinline__ uint64_t smem_desc_k32(uint32_t saddr) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((saddr >> 4) & 0x3FFFu);
+  d |= static_cast<uint64_t>(1u) << 16;
+  d |= static_cast<uint64_t>(256u >> 4) << 32;
+  d |= static_cast<uint64_t>(1u) << 46;
+  d |= static_cast<uint64_t>(6u) << 61;
+  return d;
+}
+
+// Barrier of the four feeding warps (the even and odd CTA have their own).
+__device__ __forceinline__ void feed_bar() { asm volatile("bar.sync 2, 128;" ::: "memory"); }
+__device__ __forceinline__ bool feed_all(bool p) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred pi, po;\n\t"
+      "setp.ne.u32 pi, %1, 0;\n\t"
+      "bar.red.and.pred po, 2, 128, pi;\n\t"
+      "selp.u32 %0, 1, 0, po;\n\t}\n"
+      : "=r"(r)
+      : "r"(static_cast<uint32_t>(p))
+      : "memory");
+  return r != 0;
+}
+
+// The adapter of token t: -1 outside the batch, and for an id out of range
+// (reported in the device status word).
+__device__ __forceinline__ int lora_id(const int32_t* ids, int T, int n, int t) {
+  if (t >= T) return -1;
+  const int id = ids[t];
+  if (id >= -1 && id < n) return id;
+  report_bad_index();
+  return -1;
+}
+
+__device__ __forceinline__ bool bf16_pair_nonfinite(uint32_t w) {
+  return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
+}
+__device__ __forceinline__ uint32_t bf16_pair_finite(uint32_t w) {
+  if ((w & 0x7f80u) == 0x7f80u) w &= 0xffff0000u;
+  if ((w & 0x7f800000u) == 0x7f800000u) w &= 0xffffu;
+  return w;
+}
+
+// What the non-finite weights of output `col` of token t's own adapter add.
+inline __device__ __noinline__ float lora_nonfinite_term(const LoraArgs& a, int t, int col) {
+  const int id = lora_id(a.ids, a.T, a.n, t);
+  if (id < 0) return 0.f;
+  const uint16_t* b = a.b_pool + (static_cast<size_t>(id) * a.d_out + col) * a.rank;
+  const uint16_t* v = a.v + static_cast<size_t>(t) * a.rp;
+  float s = 0.f;
+  for (int r = 0; r < a.rank; ++r)
+    if ((b[r] & 0x7f80u) == 0x7f80u) s += bf16_bits_to_f32(v[r]) * bf16_bits_to_f32(b[r]);
+  return s;
+}
+
+// Shared state of the feed (barriers, the tile's adapter list, messages).
+template <bool ON>
+struct LoraShared {};
+
+template <>
+struct LoraShared<true> {
+  uint64_t full[kLoraRing], empty[kLoraRing], landed[kLoraRing];
+  uint32_t msg[kLoraRing];        // kLoraData | kLoraLast | kLoraPoison of the slice (even CTA)
+  uint32_t msg_peer[kLoraRing];   // the odd CTA's kLoraPoison
+  uint32_t bad[kLoraRing];
+  uint32_t poison[2];
+  uint32_t heads[8];
+  alignas(16) int32_t id[256];    // read 16 bytes at a time
+  uint8_t list[256];              // rows at which an adapter occurs first
+
+  // full: one arrival of each CTA's feed (`ctas`); landed: the TMA's bytes
+  __device__ __forceinline__ void init(int ctas = 2) {
+    for (int s = 0; s < kLoraRing; ++s) {
+      mbar_init(&full[s], ctas);
+      mbar_init(&empty[s], 1);
+      mbar_init(&landed[s], 1);
+      msg_peer[s] = 0;
+      bad[s] = 0;
+    }
+    poison[0] = poison[1] = 0;
+  }
+};
+
+// Lists the distinct adapters of `ROWS` (128 or 256) tile rows in the order of
+// their first row: ls.id and ls.list are set, the count is returned.  Called by
+// the 128 feeding threads; e = thread.  i0 / i1: the ids of rows e and e + 128.
+template <int ROWS>
+__device__ __forceinline__ int lora_list(LoraShared<true>& ls, int e, int i0, int i1) {
+  feed_bar();                     // the previous tile's list is no longer read
+  ls.id[e] = i0;
+  if (ROWS == 256) ls.id[e + 128] = i1;
+  feed_bar();
+  const int w = e >> 5, lane = e & 31;
+#pragma unroll
+  for (int half = 0; half < ROWS / 128; ++half) {
+    const int id = half ? i1 : i0;
+    const int wrow = half * 128 + w * 32;              // first row of this warp's 32
+    bool head = (__ffs(__match_any_sync(0xffffffffu, id)) - 1) == lane && id >= 0;
+    if (head)
+      for (int j = 0; j < wrow && head; j += 4) {
+        const int4 o = *reinterpret_cast<const int4*>(&ls.id[j]);
+        head = o.x != id && o.y != id && o.z != id && o.w != id;
+      }
+    const uint32_t m = __ballot_sync(0xffffffffu, head);
+    if (lane == 0) ls.heads[half * 4 + w] = m;
+  }
+  feed_bar();
+  int n = 0;
+#pragma unroll
+  for (int k = 0; k < ROWS / 32; ++k) {
+    const uint32_t m = ls.heads[k];
+    if ((k & 3) == w && (m >> lane & 1u)) ls.list[n + __popc(m & ((1u << lane) - 1u))] = static_cast<uint8_t>(k * 32 + lane);
+    n += __popc(m);
+  }
+  feed_bar();
+  return n;
+}
+
+// Position in the ring of slice buffers.
+struct LoraRing {
+  uint32_t count = 0;             // slices passed so far
+};
+
+// Feeds one tile's slices: those with index j = first, first + stride, ... of
+// the list's adapters x rank / 16.  Row `e` of the v slice is token `tok` when
+// e < NV (its adapter `mine`); the slice of B holds NB rows from output row n0.
+// v_at / b_at: byte offsets of the two operands in a ring buffer.  `send` hands
+// a finished slice on: send(slot, last, poison), by thread 0.
+template <int NV, int NB, typename Send>
+__device__ __forceinline__ bool lora_feed(const LoraArgs& a, LoraShared<true>& ls, LoraRing& ring, uint8_t* ext,
+                                          uint32_t v_at, uint32_t b_at, uint32_t buf_bytes, int e, int n_list,
+                                          int first, int stride, int tok, int mine, int n0, Send send) {
+  const int per = a.rp >> 4;
+  const int total = n_list * per;
+  const int cnt = total > first ? (total - first - 1) / stride + 1 : 0;
+  const uint32_t base = ring.count;
+  auto issue = [&](int j) -> bool {        // thread 0: the slice of B into its buffer
+    const uint32_t c = base + j, slot = c % kLoraRing;
+    if (!mbar_wait_cl(&ls.empty[slot], ((c / kLoraRing) & 1u) ^ 1u)) return false;
+    const int sl = first + j * stride, li = sl / per;
+    mbar_arrive_expect_tx(&ls.landed[slot], NB * 32);
+    tma_load_3d(ext + slot * buf_bytes + b_at, &a.b, &ls.landed[slot], (sl - li * per) * 16, n0, ls.id[ls.list[li]]);
+    return true;
+  };
+  bool ok = true;
+  if (e == 0)
+    for (int j = 0; j < 2 && j < cnt && ok; ++j) ok = issue(j);
+  const uint4* vrow = reinterpret_cast<const uint4*>(a.v + static_cast<size_t>(tok) * a.rp);
+  for (int j = 0; j < cnt; ++j) {
+    const uint32_t c = base + j, slot = c % kLoraRing, phase = (c / kLoraRing) & 1u;
+    const int sl = first + j * stride, li = sl / per, k = sl - li * per;
+    const int id = ls.id[ls.list[li]];
+    uint4 v0 = make_uint4(0, 0, 0, 0), v1 = v0;
+    if (e < NV && mine == id) { v0 = vrow[2 * k]; v1 = vrow[2 * k + 1]; }
+    if (e == 0 && ok && j + 2 < cnt) ok = issue(j + 2);
+    ok = ok && mbar_wait_cl(&ls.empty[slot], phase ^ 1u);
+    uint8_t* buf = ext + slot * buf_bytes;
+    if (ok && e < NV) {
+      const int sw = (e >> 2) & 1;
+      *reinterpret_cast<uint4*>(buf + v_at + e * 32 + sw * 16) = v0;
+      *reinterpret_cast<uint4*>(buf + v_at + e * 32 + (sw ^ 1) * 16) = v1;
+    }
+    ok = ok && mbar_wait_cl(&ls.landed[slot], phase);
+    if (ok && e < NB) {
+      // both halves of the row: their places do not matter for the check
+      uint4* p = reinterpret_cast<uint4*>(buf + b_at + e * 32);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint4 w = p[h];
+        if (bf16_pair_nonfinite(w.x) || bf16_pair_nonfinite(w.y) || bf16_pair_nonfinite(w.z) || bf16_pair_nonfinite(w.w)) {
+          p[h] = make_uint4(bf16_pair_finite(w.x), bf16_pair_finite(w.y), bf16_pair_finite(w.z), bf16_pair_finite(w.w));
+          ls.bad[slot] = 1;
+        }
+      }
+    }
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    if (!feed_all(ok)) return false;
+    if (e == 0) {
+      const bool bad = ls.bad[slot] != 0;
+      ls.bad[slot] = 0;
+      send(slot, j + 1 == cnt, bad);
+    }
+  }
+  ring.count = base + cnt;
+  return true;
+}
+
+}  // namespace ftm

@@ -459,6 +459,97 @@ const char* ftm_last_warning(void);
 ftm_status ftm_moe_layer_forward_noalloc(const ftm_layer_desc* L, const ftm_layer_weights* W, const void* x,
                                          int32_t T, void* out, void* stream);
 
+/* ---- the dense projections around the routed experts ---------------------- */
+
+/* Activation of a gated feed-forward block. */
+typedef enum ftm_act {
+  FTM_ACT_SILU = 0,          /* z * sigmoid(z) */
+  FTM_ACT_GELU_TANH = 1      /* z/2 * (1 + tanh(sqrt(2/pi) * (z + 0.044715 z^3))) */
+} ftm_act;
+
+/* The dense gated feed-forward block (an MoE model's leading dense layers; its
+ * shared expert by itself), with what its backward pass needs:
+ *   g = x Wg^T, u = x Wu^T, h = act(g) * u, y = h Wd^T
+ * Both projections, the activation and the product are one kernel, the down
+ * projection a second.  The pages' engine loads and serves; the backward pass
+ * (fine-tuning the dense part on the same box) has no counterpart there.
+ *   L          the block's shape and weight format: d, I and wdtype are used (a
+ *              valid descriptor with any E, k, S).  FTM_BF16 only: others return
+ *              FTM_ERR_UNSUPPORTED (a quantised or fp32 bank's forward pass is
+ *              ftm_expert_ffn with one expert)
+ *   act        ftm_act
+ *   x, y       device bf16 [T][d]; y must not overlap x
+ *   bank       device, one bank (layout from ftm_get_bank_layout)
+ *   pre        device bf16 [T][2I] or NULL: receives g (columns 0..I-1) and u
+ *              (I..2I-1) for ftm_gated_ffn_backward.  y does not depend on it
+ *              beyond the order of its sums
+ *   workspace  device, >= ftm_gated_ffn_workspace_bytes(L, T) bytes, 256-aligned
+ * T = 0 is a no-op.  Device pointers are 16-byte aligned and lie on the current
+ * device, where `stream` belongs; anything else is refused.  No host
+ * synchronisation; the launches may be captured into a CUDA graph.  Calls that
+ * share a workspace must be ordered. */
+ftm_status ftm_gated_ffn(const ftm_layer_desc* L, int32_t act, const void* x, int32_t T, const void* bank, void* pre,
+                         void* y, void* workspace, size_t ws_bytes, void* stream);
+size_t ftm_gated_ffn_workspace_bytes(const ftm_layer_desc* L, int32_t T);
+
+/* Its backward pass, from the g and u kept by ftm_gated_ffn:
+ *   dh = dy Wd;  dg = dh * u * act'(g);  du = dh * act(g);  h = act(g) * u
+ *   dx = dg Wg + du Wu;  dWg = dg^T x;  dWu = du^T x;  dWd = dy^T h
+ *   L, act, x, T, bank   as in the forward call
+ *   pre        device bf16 [T][2I] from the forward call (read)
+ *   dy         device bf16 [T][d]
+ *   dx         device bf16 [T][d], or NULL when the input needs no gradient
+ *   dbank      device bf16, one bank: the gradients of w_gu and w_d in the
+ *              bank's own layout, overwritten (not added to), or NULL when the
+ *              weights are frozen.  dx and dbank must not both be NULL; neither
+ *              may overlap another buffer of the call
+ *   workspace  device, >= ftm_gated_ffn_backward_workspace_bytes(L, T) bytes,
+ *              256-aligned
+ * Sums are fp32 in a fixed order (the same call gives the same bits); dg, du
+ * and h are rounded to bf16 between the two launches.  T = 0 sets the weights'
+ * gradients to zero.  Otherwise as ftm_gated_ffn. */
+ftm_status ftm_gated_ffn_backward(const ftm_layer_desc* L, int32_t act, const void* x, int32_t T, const void* bank,
+                                  const void* pre, const void* dy, void* dx, void* dbank, void* workspace,
+                                  size_t ws_bytes, void* stream);
+size_t ftm_gated_ffn_backward_workspace_bytes(const ftm_layer_desc* L, int32_t T);
+
+/* A projection shared by many requests, each with its own low-rank adapter.
+ * Limits: d_in, d_out multiples of 8; rank a multiple of 8 in [8, 128] (pad a
+ * smaller adapter's rows of A and columns of B with zeros); 1 <= n_adapters <= 65536. */
+typedef struct ftm_lora_desc {
+  int32_t d_in;
+  int32_t d_out;
+  int32_t n_adapters;   /* entries of the adapter pools */
+  int32_t rank;         /* rank of every entry */
+  int32_t wdtype;       /* FTM_BF16 (others: FTM_ERR_UNSUPPORTED) */
+  int32_t reserved;     /* must be 0 */
+} ftm_lora_desc;
+
+/*   y[t] = x[t] W^T + s[a] (x[t] A[a]^T) B[a]^T,   a = adapter_ids[t]
+ * Tokens of any requests may be mixed in one call, in any order (decode batches,
+ * packed prompts); batches in which a request's tokens are adjacent are faster.
+ *   x           device bf16 [T][d_in], rows ldx elements apart (ldx >= d_in, a multiple of 8)
+ *   w           device bf16 [d_out][d_in] row-major, the shared projection
+ *   lora_a      device bf16 [n_adapters][rank][d_in]
+ *   lora_b      device bf16 [n_adapters][d_out][rank]
+ *   scale       device fp32 [n_adapters] (alpha / rank), or NULL (1)
+ *   adapter_ids device int32 [T]: the token's entry of the pools, or -1 for the
+ *               shared projection alone.  An id outside [-1, n_adapters) counts
+ *               as -1 and sets the device status word to 2
+ *   y           device bf16 [T][d_out], rows ldy elements apart (ldy >= d_out, a
+ *               multiple of 8); what lies between the rows is not written.  y
+ *               must not overlap an input
+ *   workspace   device, >= ftm_lora_workspace_bytes(D, T) bytes, 256-aligned
+ * x A^T is summed in fp32, scaled and rounded to bf16; both products are then
+ * added in one fp32 accumulator and rounded once.  A token's result depends on
+ * its own row and its own adapter alone: infinities and NaN of other requests'
+ * rows or adapters do not reach it.  Deterministic.  T = 0 is a no-op.
+ * Pointers, streams, capture and workspaces as ftm_gated_ffn. */
+ftm_status ftm_lora_linear(const ftm_lora_desc* D, const void* x, int64_t ldx, int32_t T, const void* w,
+                           const void* lora_a, const void* lora_b, const float* scale, const int32_t* adapter_ids,
+                           void* y, int64_t ldy, void* workspace, size_t ws_bytes, void* stream);
+size_t ftm_lora_workspace_bytes(const ftm_lora_desc* D, int32_t T);
+
 /* Measurement hook.  Kernel ids of the path, in launch order. */
 typedef enum ftm_kernel_id {
   FTM_K_ROUTE = 0,      /* router + gating */
