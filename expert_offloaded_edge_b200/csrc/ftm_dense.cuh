@@ -147,8 +147,10 @@ struct DenseShape {
   static constexpr uint32_t kStage = kDABytes + kBBytes;
   static constexpr int kSlots = LORA ? 2 : 3;                      // staging slots per epilogue warp
   static constexpr uint32_t kStaging = 4 * kSlots * kDSlotBytes;
-  static constexpr uint32_t kExt = LORA ? kLoraRing * (128 * 32 + BN / 2 * 32) : 0;
-  static constexpr int kStages = BN == 256 ? 5 : 6;
+  static constexpr int kGroup = 2;                                 // adapter slices per message
+  static constexpr uint32_t kBuf = 128 * 32 + BN / 2 * 32;         // a slice of v and one of B[a]
+  static constexpr uint32_t kExt = LORA ? kLoraRing * kGroup * kBuf : 0;
+  static constexpr int kStages = BN == 256 ? 5 : LORA ? 6 : 7;
   static constexpr size_t kSmem = 1024 + static_cast<size_t>(kStages) * kStage + kStaging + kExt;
   static constexpr int kThreads = LORA ? 320 : 192;
 };
@@ -264,17 +266,17 @@ __global__ void __launch_bounds__(DenseShape<BN, LORA>::kThreads, 1)
           if (++stage == kStages) { stage = 0; phase ^= 1u; }
         }
         if constexpr (LORA) {
-          // the adapters' K range: one 16-deep slice per message until the tile's last
+          // the adapters' K range, message by message until the tile's last
           uint32_t poison = 0;
           bool last = false;
           while (ok && !last) {
             if (!mbar_wait_cl(&ls.full[es], ephase)) { ok = false; break; }
             tc_fence_after();
-            const uint32_t msg = ls.msg[es];
+            const uint32_t msg = ls.msg[es], n = msg & kLoraCount;
             last = (msg & kLoraLast) != 0;
-            if (msg & kLoraData) {
-              poison |= (msg | ls.msg_peer[es]) & kLoraPoison;
-              const uint32_t sv = smem_u32(ext + es * (128 * 32 + BN / 2 * 32));
+            if (n) poison |= (msg | ls.msg_peer[es]) & kLoraPoison;
+            for (uint32_t s = 0; s < n; ++s) {
+              const uint32_t sv = smem_u32(ext + (es * S::kGroup + s) * S::kBuf);
               umma2_f16(d, smem_desc_k32(sv), smem_desc_k32(sv + 128 * 32), idesc_bf16_f32(256, BN), 1u);
             }
             umma2_commit_both(&ls.empty[es]);
@@ -380,13 +382,7 @@ __global__ void __launch_bounds__(DenseShape<BN, LORA>::kThreads, 1)
                 for (int e = 0; e < 2; ++e) {
                   const float z = __uint_as_float(e ? gw[j] & 0xffff0000u : gw[j] << 16);
                   const float u = __uint_as_float(e ? uw[j] & 0xffff0000u : uw[j] << 16);
-                  const float dh = v[2 * j + e];
-                  float s, zq;
-                  act_parts(z, g.act, s, zq);
-                  const float a = z * s;
-                  dg[e] = dh * u * fmaf(zq * s, 1.f - s, s);
-                  du[e] = dh * a;
-                  h[e] = a * u;
+                  act_gradient(z, u, v[2 * j + e], g.act, dg[e], du[e], h[e]);
                 }
                 wg[j] = pack_bf16(dg[0], dg[1]);
                 wu[j] = pack_bf16(du[0], du[1]);
@@ -428,10 +424,11 @@ __global__ void __launch_bounds__(DenseShape<BN, LORA>::kThreads, 1)
         const DenseTile ti = dense_decode(g, t);
         const int m0 = ti.m * kDTileM;
         const int i0 = lora_id(L.ids, L.T, L.n, m0 + e), i1 = lora_id(L.ids, L.T, L.n, m0 + 128 + e);
-        const int nl = lora_list<256>(ls, e, i0, i1);
-        auto send = [&](uint32_t slot, bool last, bool bad) {
+        int at;
+        const int nl = lora_list<256>(ls, e, i0, i1, static_cast<int>(rank), at);
+        auto send = [&](uint32_t slot, uint32_t n, bool last, bool bad) {
           if (leader) {
-            ls.msg[slot] = kLoraData | (last ? kLoraLast : 0u) | (bad ? kLoraPoison : 0u);
+            ls.msg[slot] = n | (last ? kLoraLast : 0u) | (bad ? kLoraPoison : 0u);
             mbar_arrive(&ls.full[slot]);
           } else {
             asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(mapa_rank(smem_u32(&ls.msg_peer[slot]), 0)),
@@ -446,7 +443,6 @@ __global__ void __launch_bounds__(DenseShape<BN, LORA>::kThreads, 1)
           ok = mbar_wait_cl(&ls.empty[slot], ((ring.count / kLoraRing) & 1u) ^ 1u);
           ok = feed_all(ok);
           if (ok && e == 0) {
-            mbar_arrive(&ls.landed[slot]);      // every use of a slot is one phase of its barriers
             if (leader) {
               ls.msg[slot] = kLoraLast;
               mbar_arrive(&ls.full[slot]);
@@ -457,9 +453,9 @@ __global__ void __launch_bounds__(DenseShape<BN, LORA>::kThreads, 1)
           ring.count += 1;
           continue;
         }
-        ok = lora_feed<128, BN / 2>(L, ls, ring, ext, 0, 128 * 32, 128 * 32 + BN / 2 * 32, e, nl, 0, 1,
-                                    m0 + static_cast<int>(rank) * 128 + e, leader ? i0 : i1,
-                                    ti.n * BN + static_cast<int>(rank) * (BN / 2), send);
+        ok = lora_feed<128, BN / 2, S::kGroup>(L, ls, ring, ext, 0, 128 * 32, S::kBuf, e, nl, 0, 1,
+                                               m0 + static_cast<int>(rank) * 128 + e, (leader ? i0 : i1) >= 0 ? at : -1,
+                                               ti.n * BN + static_cast<int>(rank) * (BN / 2), [] {}, send);
       }
     }
   }

@@ -123,7 +123,7 @@ __global__ void __launch_bounds__(256) simt_gemm2_kernel(const float* __restrict
 // ---------------------------------------------------------------------------
 constexpr int kBK = 64;               // K per stage: 64 bf16 = one 128-byte swizzle row
 
-template <int BN, bool GATED, int ACT = FTM_ACT_SILU>
+template <int BN, bool GATED>
 __global__ void __launch_bounds__(kTcThreads, 1)
     ffn_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmAsh,
                   const __grid_constant__ CUtensorMap tmB, const int32_t* __restrict__ offsets,
@@ -302,7 +302,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
           if (c0 + j < valid) {
-            const float v = GATED ? (ACT == FTM_ACT_SILU ? silu(a[j]) : act_value(a[j], ACT)) * b[j] : a[j];
+            const float v = GATED ? silu(a[j]) * b[j] : a[j];
             const __nv_bfloat16 hv = __float2bfloat16_rn(v);
             obase[static_cast<size_t>(c0 + j) * ld_out] = *reinterpret_cast<const uint16_t*>(&hv);
           }
@@ -341,7 +341,7 @@ static long tile_bound(int P, int T, int E, int has_shared, int BN, int MT) {
   return (routed + (has_shared ? (T + BN - 1) / BN : 0)) * MT;
 }
 
-template <int BN, bool GATED, int ACT = FTM_ACT_SILU>
+template <int BN, bool GATED>
 static cudaError_t launch_tc(const CUtensorMap& mA, const CUtensorMap& mAsh, const CUtensorMap& mB,
                              const FfnArgs& a, int K, int Nw, int up_row0, uint16_t* out, int ld_out,
                              cudaStream_t st) {
@@ -351,7 +351,7 @@ static cudaError_t launch_tc(const CUtensorMap& mA, const CUtensorMap& mAsh, con
   const int P = a.T * a.k;
   const long tiles = tile_bound(P, a.T, a.E, a.has_shared, BN, Nw / 128);
   const int KB = K / kBK;
-  auto kern = ffn_tc_kernel<BN, GATED, ACT>;
+  auto kern = ffn_tc_kernel<BN, GATED>;
   auto stages_for = [](int ks) {
     const int red_bytes = (ks - 1) * 128 * kRedStride * 4;
     const int s = (200 * 1024 - 1024 - red_bytes) / static_cast<int>(kStageBytes);
@@ -431,18 +431,18 @@ static cudaError_t launch_tc(const CUtensorMap& mA, const CUtensorMap& mAsh, con
                             up_row0, out, ld_out, stages));
 }
 
-template <bool GATED, int ACT = FTM_ACT_SILU>
+template <bool GATED>
 static cudaError_t launch_tc_bn(int bn, const CUtensorMap& mA, const CUtensorMap& mAsh, const CUtensorMap& mB,
                                 const FfnArgs& a, int K, int Nw, int up_row0, uint16_t* out, int ld_out,
                                 cudaStream_t st) {
   switch (bn) {
-    case 16: return launch_tc<16, GATED, ACT>(mA, mAsh, mB, a, K, Nw, up_row0, out, ld_out, st);
-    case 32: return launch_tc<32, GATED, ACT>(mA, mAsh, mB, a, K, Nw, up_row0, out, ld_out, st);
-    case 64: return launch_tc<64, GATED, ACT>(mA, mAsh, mB, a, K, Nw, up_row0, out, ld_out, st);
-    case 128: return launch_tc<128, GATED, ACT>(mA, mAsh, mB, a, K, Nw, up_row0, out, ld_out, st);
+    case 16: return launch_tc<16, GATED>(mA, mAsh, mB, a, K, Nw, up_row0, out, ld_out, st);
+    case 32: return launch_tc<32, GATED>(mA, mAsh, mB, a, K, Nw, up_row0, out, ld_out, st);
+    case 64: return launch_tc<64, GATED>(mA, mAsh, mB, a, K, Nw, up_row0, out, ld_out, st);
+    case 128: return launch_tc<128, GATED>(mA, mAsh, mB, a, K, Nw, up_row0, out, ld_out, st);
     default:
       // 256-token tiles only without the gate/up pair (TMEM holds 2 x 256 fp32 columns)
-      if (GATED) return launch_tc<128, GATED, ACT>(mA, mAsh, mB, a, K, Nw, up_row0, out, ld_out, st);
+      if (GATED) return launch_tc<128, GATED>(mA, mAsh, mB, a, K, Nw, up_row0, out, ld_out, st);
       return launch_tc<256, false>(mA, mAsh, mB, a, K, Nw, up_row0, out, ld_out, st);
   }
 }
@@ -514,36 +514,6 @@ const char* launch_expert_ffn(const FfnArgs& a, cudaStream_t st, cudaError_t* ce
   prof_mark(FTM_K_GEMM2, st, true);
   if (*cerr != cudaSuccess) return "tensor-core gemm2 launch failed";
   return nullptr;
-}
-
-// The dense gated block (see ftm_dense.cu) for few tokens: the same kernels with
-// the shared group alone (E = 0), straight from x, without the gather.
-const char* launch_gated_ffn_small(int act, const void* x, int T, int d, int I, const void* bank, size_t w_d_off,
-                                   void* h, void* y, cudaStream_t st, cudaError_t* cerr) {
-  FfnArgs a = {};
-  a.d = d;
-  a.I = I;
-  a.T = T;
-  a.has_shared = 1;
-  const int bn = ffn_token_tile(T, 1);
-  const uint8_t* w = static_cast<const uint8_t*>(bank);
-  CUtensorMap mA1, mB1, mA2, mB2;
-  if (!make_map_bf16(&mA1, w, d, 2ull * I, 2ull * d, 0, 0, 128) ||
-      !make_map_bf16(&mA2, w + w_d_off, I, d, 2ull * I, 0, 0, 128) ||
-      !make_map_bf16(&mB1, x, d, T, 2ull * d, 0, 0, bn) || !make_map_bf16(&mB2, h, I, T, 2ull * I, 0, 0, bn)) {
-    *cerr = cudaSuccess;
-    return "cuTensorMapEncodeTiled failed";
-  }
-  uint16_t* hp = static_cast<uint16_t*>(h);
-  prof_mark(FTM_K_GEMM1, st, false);
-  *cerr = act == FTM_ACT_SILU ? launch_tc_bn<true>(bn, mA1, mA1, mB1, a, d, I, I, hp, I, st)
-                              : launch_tc_bn<true, FTM_ACT_GELU_TANH>(bn, mA1, mA1, mB1, a, d, I, I, hp, I, st);
-  prof_mark(FTM_K_GEMM1, st, true);
-  if (*cerr != cudaSuccess) return "gate/up launch failed";
-  prof_mark(FTM_K_GEMM2, st, false);
-  *cerr = launch_tc_bn<false>(bn, mA2, mA2, mB2, a, I, d, 0, static_cast<uint16_t*>(y), d, st);
-  prof_mark(FTM_K_GEMM2, st, true);
-  return *cerr == cudaSuccess ? nullptr : "down launch failed";
 }
 
 }  // namespace ftm

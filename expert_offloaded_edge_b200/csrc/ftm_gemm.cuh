@@ -40,6 +40,16 @@ __device__ __forceinline__ float act_value(float z, int act) {
   return z * s;
 }
 
+// dg = dh u act'(z), du = dh act(z), h = act(z) u.
+__device__ __forceinline__ void act_gradient(float z, float u, float dh, int act, float& dg, float& du, float& h) {
+  float s, zq;
+  act_parts(z, act, s, zq);
+  const float a = z * s;
+  dg = dh * u * fmaf(zq * s, 1.f - s, s);
+  du = dh * a;
+  h = a * u;
+}
+
 // ---- thread-block cluster helpers ------------------------------------------
 __device__ __forceinline__ uint32_t cluster_nranks() {
   uint32_t r;

@@ -5,26 +5,47 @@
 //      operand type of the second product; a relative 2^-9 of the adapter's
 //      part of y alone);
 //   2. the projection over K = d_in and the adapters' K range (ftm_lora.cuh):
-//      lora_proj_kernel below for few tokens (bound by the bytes of W: weights
-//      on the MMA's M side, split over a cluster along K), the CTA-pair engine
-//      of ftm_dense.cuh for many.
-#include "ftm_dense.cuh"
+//      ftm_proj.cuh for few tokens (bound by the bytes of W), the CTA-pair
+//      engine of ftm_dense.cuh for many.
+#include "ftm_proj.cuh"
 
 namespace ftm {
 
 // ---------------------------------------------------------------------------
-// v = s (x A^T).  A block takes 16 MI tokens and one share of K (a cluster of
+// v = s (x A^T).  A block takes MT tokens and one share of K (a cluster of
 // blocks splits K) and walks over the adapters that occur among its tokens:
-// tensor-core products of all its rows with 32 rows of A[a] at a time, kept for
-// the tokens whose adapter it is.  blockIdx.y shares out the adapters of a tile,
-// since a decode batch may bring 16 of them to 16 tokens.  mma.sync on purpose:
-// the product reads A once per tile and does 2 rank flops per value of x, far
-// below the tensor rate, and takes any mixture of adapters without a layout.
-// Each thread loads 16 consecutive bytes of a row per operand: the depths of
-// one 32-deep step are dealt to the two MMAs in the same order on both sides.
+// tensor-core products of all its rows with the rows of A[a], kept for the
+// tokens whose adapter it is.  blockIdx.y shares out the adapters of a tile,
+// since a decode batch may bring 16 of them to 16 tokens.
+//
+// Within a window of 512, tokens whose adapters change often are tiled in the
+// order of their adapters, so that A[a] is read once per MT tokens of adapter a
+// however the requests are mixed (every block ranks its window's ids by
+// counting: 1.4 us at 64 tokens, 3.3 at 256); packed prompts are tiled as they
+// come.
+//
+// mma.sync on purpose: the product reads x and A once and does 2 rank flops per
+// value of x, far below the tensor rate, and takes any mixture of adapters
+// without a layout.
 // ---------------------------------------------------------------------------
-constexpr int kShrinkWarps = 8;
-constexpr int kShrinkCols = 32;                // rows of A (columns of v) per pass
+// Weights up to this size are asked into L2 ahead of their use (half of the 126 MB).
+constexpr size_t kPrefetchBytes = 64u << 20;
+
+constexpr int kShrinkThreads = 256;
+constexpr int kShrinkWindow = 512;
+
+struct ShrinkArgs {
+  const uint16_t* x;
+  int64_t ldx;
+  int T, K;
+  const uint16_t* a_pool;
+  const float* scale;
+  const int32_t* ids;
+  int n, rank, rp;
+  uint16_t* v;
+  const uint8_t* w;         // the projection's weights, prefetched (w_bytes 0: not wanted)
+  size_t w_bytes;
+};
 
 __device__ __forceinline__ void mma_bf16_16816(float* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                                uint32_t b1) {
@@ -35,332 +56,373 @@ __device__ __forceinline__ void mma_bf16_16816(float* c, uint32_t a0, uint32_t a
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-template <int MI, int KS>
-__global__ void __launch_bounds__(kShrinkWarps * 32)
-    lora_shrink_kernel(const uint16_t* __restrict__ x, int64_t ldx, int T, int K, const uint16_t* __restrict__ a_pool,
-                       const float* __restrict__ scale, const int32_t* __restrict__ ids, int n, int rank, int rp,
-                       uint16_t* __restrict__ v) {
-  constexpr int MT = 16 * MI;
-  constexpr int kOut = MT * kShrinkCols;
-  __shared__ float red[kShrinkWarps][kOut];
-  __shared__ float part[KS > 1 ? 2 * KS * kOut : 1];   // rank 0: the ranks' sums, by pass parity
-  __shared__ int32_t s_id[MT];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int g = lane >> 2, tq = lane & 3;
-  const int kr = KS > 1 ? static_cast<int>(cluster_rank()) : 0;
-  const int m0 = static_cast<int>(blockIdx.x / KS) * MT;
+// A block's tile: the tokens in its places and the distinct adapters among them.
+template <int MT>
+struct ShrinkTile {
+  __align__(16) uint32_t key[kShrinkWindow];
+  int32_t id[MT], tok[MT];                             // adapter and token of a place; tok -1: none
+  int32_t list[MT];                                    // the adapters of its runs
+  uint32_t heads[(MT + 31) / 32];                      // places at which an adapter begins
+};
+
+// Fills the tile at place m0 of the window that starts at token `base`, after
+// the wait for the launch before; returns the length of its list.  Ends with a
+// barrier of the cluster.
+template <int MT>
+__device__ __forceinline__ int shrink_tile(const ShrinkArgs& p, ShrinkTile<MT>& s, int base, int m0, int ks) {
+  // The projection's weights into L2 while v is computed, every block its share.
+  if (p.w_bytes && threadIdx.x == 0) {
+    const size_t blocks = static_cast<size_t>(gridDim.x) * gridDim.y, b = static_cast<size_t>(blockIdx.y) * gridDim.x + blockIdx.x;
+    const size_t share = ((p.w_bytes + blocks - 1) / blocks + 15) & ~static_cast<size_t>(15);
+    const size_t lo = b * share, hi = lo + share < p.w_bytes ? lo + share : p.w_bytes;
+    for (size_t at = lo; at < hi; at += 16384) {
+      const uint32_t bytes = static_cast<uint32_t>(hi - at < 16384 ? hi - at : 16384);
+      asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p.w + at), "r"(bytes) : "memory");
+    }
+  }
   pdl_wait();
   pdl_trigger();
-  if (threadIdx.x < 32) {
-    const int id = lane < MT ? lora_id(ids, T, n, m0 + lane) : -1;
-    if (lane < MT) s_id[lane] = id;
+  // Every adapter (n for none) and token of the window make one key.  Where the ids change often (a mixed
+  // decode batch) the places are in the order of the keys: a token's place is the number of lower keys.
+  const int Tw = min(kShrinkWindow, p.T - base), Tp = (Tw + 3) & ~3;
+  int changes = 0;
+  for (int t = threadIdx.x; t < Tp; t += kShrinkThreads) {
+    const int id = lora_id(p.ids, p.T, p.n, t < Tw ? base + t : p.T);
+    s.key[t] = t < Tw ? static_cast<uint32_t>(id < 0 ? p.n : id) * kShrinkWindow + t : 0xffffffffu;
+  }
+  if (threadIdx.x < MT) s.id[threadIdx.x] = s.tok[threadIdx.x] = -1;
+  __syncthreads();
+  for (int t = threadIdx.x; t + 1 < Tw; t += kShrinkThreads)
+    changes += s.key[t] / kShrinkWindow != s.key[t + 1] / kShrinkWindow;
+  const bool mixed = Tw > MT && __syncthreads_count(changes) * 16 > Tw;
+  for (int t = threadIdx.x; t < Tw; t += kShrinkThreads) {
+    const uint32_t me = s.key[t];
+    int place = mixed ? 0 : t;
+    if (mixed) {
+#pragma unroll 8
+      for (int o = 0; o < Tp; o += 4) {
+        const uint4 k = *reinterpret_cast<const uint4*>(&s.key[o]);
+        place += (k.x < me) + (k.y < me) + (k.z < me) + (k.w < me);
+      }
+    }
+    if (place >= m0 && place < m0 + MT) {
+      const int id = static_cast<int>(me / kShrinkWindow);
+      s.id[place - m0] = id < p.n ? id : -1;
+      s.tok[place - m0] = base + t;
+    }
   }
   __syncthreads();
-  if (KS > 1) cluster_sync_all();       // every rank runs before the first remote store
-  // distinct adapters: bit i of `heads` where token i is the first of its adapter
-  const int my = lane < MT ? s_id[lane] : -1;
-  uint32_t heads = __ballot_sync(0xffffffffu, (__ffs(__match_any_sync(0xffffffffu, my)) - 1) == lane && my >= 0);
-  const int steps = (K + 31) / 32;
-  const int c_lo = steps * kr / KS, c_hi = steps * (kr + 1) / KS;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int i = threadIdx.x;
+  int id = -1;
+  bool head = false;
+  if (i < MT) {
+    id = s.id[i];
+    head = id >= 0 && (i == 0 || s.id[i - 1] != id);   // an adapter of two runs is listed, and computed, twice
+  }
+  if (i < (MT + 31) / 32 * 32) {
+    const uint32_t m = __ballot_sync(0xffffffffu, head);
+    if (lane == 0) s.heads[warp] = m;
+  }
+  __syncthreads();
+  int n = 0;
+#pragma unroll
+  for (int w = 0; w < (MT + 31) / 32; ++w) {
+    if (w == warp && head) s.list[n + __popc(s.heads[w] & ((1u << lane) - 1u))] = id;
+    n += __popc(s.heads[w]);
+  }
+  if (ks > 1) cluster_sync_all();       // also: every rank runs before the first remote store
+  else __syncthreads();
+  return n;
+}
+
+// A pass's outputs, MT places x NC columns in pieces of 8 columns (16 bytes of
+// v): `sums(at, f)` gives this block's sums of the piece that starts at output
+// `at`; the cluster's ranks each add up their share of the pieces in rank order,
+// scale, round and store.  column(c, r): the adapter of the piece at column c
+// (-1: none), and its place r in v.
+template <int MT, int NC, typename Sums, typename Column>
+__device__ __forceinline__ void shrink_store(const ShrinkArgs& p, const ShrinkTile<MT>& s, float* part, int ks, int kr,
+                                             Sums sums, Column column) {
+  constexpr int kPieces = MT * NC / 8;
+  const int own = (kPieces + ks - 1) / ks;
+  if (ks > 1) {
+    for (int at = threadIdx.x; at < kPieces; at += kShrinkThreads) {
+      float f[8];
+      sums(at * 8, f);
+      const int owner = at / own;
+      const uint32_t to = mapa_rank(smem_u32(part + (kr * own + at - owner * own) * 8), owner);
+      st_cluster_v4(to, f[0], f[1], f[2], f[3]);
+      st_cluster_v4(to + 16, f[4], f[5], f[6], f[7]);
+    }
+    cluster_sync_all();
+  }
+  for (int o = threadIdx.x; o < own; o += kShrinkThreads) {
+    const int at = kr * own + o;
+    if (at >= kPieces) break;
+    const int i = at * 8 / NC;
+    int r;
+    const int id = column(at * 8 % NC, r);
+    if (id < 0 || s.tok[i] < 0 || s.id[i] != id) continue;
+    const float scale = p.scale ? p.scale[id] : 1.f;
+    float f[8] = {};
+    if (ks > 1) {
+      for (int q = 0; q < ks; ++q) {
+        const float4* u = reinterpret_cast<const float4*>(part + (q * own + o) * 8);
+        const float4 a = u[0], b = u[1];
+        f[0] += a.x; f[1] += a.y; f[2] += a.z; f[3] += a.w;
+        f[4] += b.x; f[5] += b.y; f[6] += b.z; f[7] += b.w;
+      }
+    } else {
+      sums(at * 8, f);
+    }
+    // rank is a multiple of 8: a piece is all rank or all padding, which is zero whatever the scale
+    uint4 w = make_uint4(0, 0, 0, 0);
+    if (r < p.rank)
+      w = make_uint4(pack_bf16(scale * f[0], scale * f[1]), pack_bf16(scale * f[2], scale * f[3]),
+                     pack_bf16(scale * f[4], scale * f[5]), pack_bf16(scale * f[6], scale * f[7]));
+    *reinterpret_cast<uint4*>(p.v + static_cast<size_t>(s.tok[i]) * p.rp + r) = w;
+  }
+  if (ks == 1) __syncthreads();         // the sums' buffer is free again
+}
+
+// Few tokens: tiles of 16, the 8 warps split the block's depth, operands straight
+// into registers.  Each thread loads 16 consecutive bytes of a row per operand:
+// the depths of one 32-deep step are dealt to the two MMAs in the same order on
+// both sides, and a warp takes two neighbouring steps (128 bytes of a row) at once.
+template <int NJ>
+struct ShrinkFew {
+  static constexpr int MT = 16, NC = 8 * NJ, kOut = MT * NC, kPart = kOut + 64;
+  static constexpr size_t kSmem = static_cast<size_t>(8 * kOut + 2 * kPart) * 4;
+};
+
+template <int NJ>
+__global__ void __launch_bounds__(kShrinkThreads, NJ == 8 ? 1 : 2) lora_shrink_few_kernel(const ShrinkArgs p) {
+  using S = ShrinkFew<NJ>;
+  constexpr int NC = S::NC, kOut = S::kOut;
+  extern __shared__ __align__(16) float s_dyn[];
+  float* red = s_dyn;                                  // [warp][place][column]
+  float* part = s_dyn + 8 * kOut;                      // [pass parity][rank][its share of the outputs]
+  __shared__ ShrinkTile<16> s;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, tq = lane & 3;
+  const int ks = static_cast<int>(cluster_nranks()), kr = static_cast<int>(cluster_rank());
+  const int n_list = shrink_tile(p, s, 0, static_cast<int>(blockIdx.x / ks) * 16, ks);
+  const int steps = (p.K + 31) / 32;
+  const int c_lo = steps * kr / ks, c_hi = steps * (kr + 1) / ks;
+  const int t0 = s.tok[g], t1 = s.tok[g + 8];
+  const uint16_t* x0 = t0 >= 0 ? p.x + t0 * p.ldx : nullptr;
+  const uint16_t* x1 = t1 >= 0 ? p.x + t1 * p.ldx : nullptr;
   int pass = 0;
-  for (int li = 0; heads; ++li) {
-    const int head = __ffs(heads) - 1;
-    heads &= heads - 1;
-    if (li % static_cast<int>(gridDim.y) != static_cast<int>(blockIdx.y)) continue;
-    const int id = s_id[head];
-    const uint16_t* A = a_pool + static_cast<size_t>(id) * rank * K;
-    for (int n0 = 0; n0 < rp; n0 += kShrinkCols, ++pass) {
-      float acc[MI][4][4] = {};
-#pragma unroll 4
-      for (int c = c_lo + warp; c < c_hi; c += kShrinkWarps) {
-        const int k = c * 32 + tq * 8;
-        uint4 xv[MI][2], av[4];
+  for (int li = blockIdx.y; li < n_list; li += gridDim.y) {
+    const int id = s.list[li];
+    const uint16_t* A = p.a_pool + static_cast<size_t>(id) * p.rank * p.K;
+    for (int n0 = 0; n0 < p.rp; n0 += NC, ++pass) {
+      float acc[NJ][4] = {};
+      for (int c2 = c_lo + 2 * warp; c2 < c_hi; c2 += 16) {
+        uint4 xv[2][2], av[2][NJ];
+        const uint4 zero = make_uint4(0, 0, 0, 0);
 #pragma unroll
-        for (int i = 0; i < MI; ++i)
+        for (int u = 0; u < 2; ++u) {
+          const int k = (c2 + u) * 32 + tq * 8;
+          const bool in = c2 + u < c_hi && k < p.K;
+          xv[u][0] = in && x0 ? __ldg(reinterpret_cast<const uint4*>(x0 + k)) : zero;
+          xv[u][1] = in && x1 ? __ldg(reinterpret_cast<const uint4*>(x1 + k)) : zero;
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int t = m0 + i * 16 + h * 8 + g;
-            xv[i][h] = t < T && k < K ? __ldg(reinterpret_cast<const uint4*>(x + t * ldx + k)) : make_uint4(0, 0, 0, 0);
+          for (int j = 0; j < NJ; ++j) {
+            const int r = n0 + j * 8 + g;
+            av[u][j] = in && r < p.rank ? __ldg(reinterpret_cast<const uint4*>(A + static_cast<size_t>(r) * p.K + k)) : zero;
           }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int r = n0 + j * 8 + g;
-          av[j] = r < rank && k < K ? __ldg(reinterpret_cast<const uint4*>(A + static_cast<size_t>(r) * K + k))
-                                    : make_uint4(0, 0, 0, 0);
         }
 #pragma unroll
-        for (int i = 0; i < MI; ++i)
+        for (int u = 0; u < 2; ++u)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            mma_bf16_16816(acc[i][j], xv[i][0].x, xv[i][1].x, xv[i][0].y, xv[i][1].y, av[j].x, av[j].y);
-            mma_bf16_16816(acc[i][j], xv[i][0].z, xv[i][1].z, xv[i][0].w, xv[i][1].w, av[j].z, av[j].w);
+          for (int j = 0; j < NJ; ++j) {
+            mma_bf16_16816(acc[j], xv[u][0].x, xv[u][1].x, xv[u][0].y, xv[u][1].y, av[u][j].x, av[u][j].y);
+            mma_bf16_16816(acc[j], xv[u][0].z, xv[u][1].z, xv[u][0].w, xv[u][1].w, av[u][j].z, av[u][j].w);
           }
       }
 #pragma unroll
-      for (int i = 0; i < MI; ++i)
+      for (int j = 0; j < NJ; ++j)
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-            *reinterpret_cast<float2*>(&red[warp][(i * 16 + h * 8 + g) * kShrinkCols + j * 8 + 2 * tq]) =
-                make_float2(acc[i][j][2 * h], acc[i][j][2 * h + 1]);
+        for (int h = 0; h < 2; ++h)
+          *reinterpret_cast<float2*>(&red[warp * kOut + (h * 8 + g) * NC + j * 8 + 2 * tq]) =
+              make_float2(acc[j][2 * h], acc[j][2 * h + 1]);
       __syncthreads();
-      float* mine = part + (pass & 1) * KS * kOut;
-      float sum[kOut / 256];
+      auto warps = [&](int at, float* f) {
 #pragma unroll
-      for (int o = 0; o < kOut / 256; ++o) {
-        const int at = o * 256 + threadIdx.x;
-        float s = 0.f;
+        for (int i = 0; i < 8; ++i) f[i] = 0.f;
 #pragma unroll
-        for (int w = 0; w < kShrinkWarps; ++w) s += red[w][at];
-        sum[o] = s;
-        if (KS > 1)
-          asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(mapa_rank(smem_u32(mine + kr * kOut + at), 0)), "f"(s)
-                       : "memory");
-      }
-      if (KS > 1) cluster_sync_all();
-      else __syncthreads();             // red is free again
-      if (kr == 0) {
-        const float sc = scale ? scale[id] : 1.f;
-#pragma unroll
-        for (int o = 0; o < kOut / 256; ++o) {
-          const int at = o * 256 + threadIdx.x;
-          const int i = at / kShrinkCols, r = n0 + at % kShrinkCols;
-          float s = sum[o];
-          if (KS > 1) {
-            s = 0.f;
-#pragma unroll
-            for (int p = 0; p < KS; ++p) s += mine[p * kOut + at];
-          }
-          if (s_id[i] == id && r < rp) {
-            // columns that pad the rank to 16 are zero whatever the scale
-            const __nv_bfloat16 b = __float2bfloat16_rn(r < rank ? sc * s : 0.f);
-            v[static_cast<size_t>(m0 + i) * rp + r] = *reinterpret_cast<const uint16_t*>(&b);
-          }
+        for (int w = 0; w < 8; ++w) {
+          const float4* u = reinterpret_cast<const float4*>(red + w * kOut + at);
+          const float4 a = u[0], b = u[1];
+          f[0] += a.x; f[1] += a.y; f[2] += a.z; f[3] += a.w;
+          f[4] += b.x; f[5] += b.y; f[6] += b.z; f[7] += b.w;
         }
-      }
+      };
+      shrink_store<16, NC>(p, s, part + (pass & 1) * S::kPart, ks, kr, warps, [&](int c, int& r) {
+        r = n0 + c;
+        return r < p.rp ? id : -1;
+      });
     }
   }
 }
 
-// ---------------------------------------------------------------------------
-// The projection for few tokens.  One cluster of ks CTAs per (128 outputs, BN
-// tokens) tile, each CTA a share of K and of the adapters' slices; the partial
-// sums meet in shared memory (CTA s sums the token columns it owns in rank
-// order, so the result does not depend on timing).  W is read once per token
-// tile; its loads are issued before the shrink's results are waited for.
-// ---------------------------------------------------------------------------
-template <int BN>
-struct ProjShape {
-  static constexpr uint32_t kBBytes = ((BN * 128 + 1023) / 1024) * 1024;
-  static constexpr uint32_t kStage = kATileBytes + kBBytes;
-  static constexpr int kStages = BN <= 32 ? 7 : BN == 64 ? 5 : 3;
-  static constexpr uint32_t kBuf = 128 * 32 + BN * 32;               // a slice of B[a] and one of v
-  static constexpr uint32_t kTmemCols = BN < 32 ? 32 : BN;
-  static size_t red_bytes(int ks) { return ks > 1 ? static_cast<size_t>(ks) * ((BN + ks - 1) / ks) * 512 : 0; }
-  static size_t smem(int ks) { return 1024 + static_cast<size_t>(kStages) * kStage + kLoraRing * kBuf + red_bytes(ks); }
+// Many tokens: tiles of 64 places and NC columns, which hold as many of the
+// tile's adapters as fit (a tile over the border of two requests takes no longer
+// than another), so that x is read once: bound by its bytes.  A ring of 128-deep
+// stages filled by cp.async (rows are gathered, so no TMA box), four warps over
+// the rows times two over each stage's depth.
+template <int NJ>
+struct ShrinkMany {
+  static constexpr int MT = 64, NC = 8 * NJ, kOut = MT * NC, kPart = kOut + 64;
+  static constexpr int kHalf = (MT + NC) * 128;                      // 64 deep of a stage
+  static constexpr int kStages = NJ == 16 ? 3 : 5;
+  static constexpr size_t kRing = static_cast<size_t>(kStages) * 2 * kHalf;
+  static constexpr size_t kSmem = kRing + static_cast<size_t>(2 * kPart) * 4;
+  static_assert(2 * kOut * 4 <= kRing, "the depth halves' sums take the ring's place");
 };
 
-template <int BN>
-__global__ void __launch_bounds__(192, 1)
-    lora_proj_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
-                     const __grid_constant__ LoraArgs a, int K, uint16_t* __restrict__ y, int64_t ldy) {
-  using S = ProjShape<BN>;
-  constexpr uint32_t kIdesc = idesc_bf16_f32(128, BN);
-  extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t full_bar[S::kStages], empty_bar[S::kStages], tfull_bar, count_bar;
-  __shared__ uint32_t tmem_holder, slices;
-  __shared__ LoraShared<true> ls;
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool in) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
+}
 
-  const uint32_t smem_base = (smem_u32(smem_raw) + 1023u) & ~1023u;
-  uint8_t* smem = smem_raw + (smem_base - smem_u32(smem_raw));
-  uint8_t* ext = smem + static_cast<size_t>(S::kStages) * S::kStage;
-  float* red = reinterpret_cast<float*>(ext + kLoraRing * S::kBuf);
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+__device__ __forceinline__ void ldmatrix_x4(uint32_t addr, uint32_t* r) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr));
+}
+
+template <int NJ>
+__global__ void __launch_bounds__(kShrinkThreads, 1) lora_shrink_many_kernel(const ShrinkArgs p) {
+  using S = ShrinkMany<NJ>;
+  constexpr int MT = S::MT, NC = S::NC, kOut = S::kOut, kStages = S::kStages;
+  extern __shared__ __align__(128) uint8_t s_ring[];
+  float* red = reinterpret_cast<float*>(s_ring);                     // [depth half][place][column], when the ring is done
+  float* part = reinterpret_cast<float*>(s_ring + S::kRing);
+  __shared__ ShrinkTile<MT> s;
+  __shared__ int32_t s_col[NJ], s_r[NJ];                             // 8 columns' adapter (-1: none) and place in v
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int wm = warp & 3, wk = warp >> 2;
   const int ks = static_cast<int>(cluster_nranks()), kr = static_cast<int>(cluster_rank());
-  const int n0 = blockIdx.y * BN, w0 = blockIdx.z * 128;
-  const int KB = (K + 63) / 64;
+  const int tile = blockIdx.x / ks;
+  constexpr int kTiles = kShrinkWindow / MT;
+  const int n_ad = shrink_tile(p, s, tile / kTiles * kShrinkWindow, tile % kTiles * MT, ks);
+  const int KB = (p.K + 127) / 128;
   const int kb0 = kr * KB / ks, kb1 = (kr + 1) * KB / ks;
-
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < S::kStages; ++s) { mbar_init(&full_bar[s], 1); mbar_init(&empty_bar[s], 1); }
-    mbar_init(&tfull_bar, 1);
-    mbar_init(&count_bar, 1);
-    ls.init(1);
-    fence_mbar_init();
-  }
-  if (warp == 1) {
-    tmem_alloc(&tmem_holder, S::kTmemCols);
-    tmem_relinquish();
-  }
-  tc_fence_before();
-  if (ks > 1) cluster_sync_all();       // every rank's shared memory may be written from here on
-  else __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem_base = tmem_holder;
-
-  if (warp == 0) {
-    // The launch before this one is always the shrink, which started this one
-    // after its own wait for everything earlier: x and W are final.
-    if (lane == 0) {
-      int stage = 0;
-      uint32_t phase = 0;
-      for (int kb = kb0; kb < kb1; ++kb) {
-        if (!mbar_wait(&empty_bar[stage], phase ^ 1u)) break;
-        mbar_arrive_expect_tx(&full_bar[stage], kATileBytes + BN * 128);
-        uint8_t* sa = smem + static_cast<size_t>(stage) * S::kStage;
-        tma_load_2d(sa, &tmW, &full_bar[stage], kb * 64, w0);
-        tma_load_2d(sa + kATileBytes, &tmX, &full_bar[stage], kb * 64, n0);
-        if (++stage == S::kStages) { stage = 0; phase ^= 1u; }
-      }
-    }
-    __syncwarp();
-  } else if (warp == 1) {
-    if (lane == 0) {
-      int stage = 0;
-      uint32_t phase = 0;
-      bool ok = true;
-      for (int kb = kb0; kb < kb1; ++kb) {
-        if (!mbar_wait(&full_bar[stage], phase)) { ok = false; break; }
-        tc_fence_after();
-        const uint32_t sa = smem_u32(smem + static_cast<size_t>(stage) * S::kStage);
+  const uint32_t ring = smem_u32(s_ring);
+  // this thread's 16-byte pieces of a stage: piece lc of each half of rows lr, lr + 32, ...
+  const int lr = threadIdx.x >> 3, lc = threadIdx.x & 7;
+  const uint16_t* xr[2];
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-          umma_f16(tmem_base, smem_desc_sw128(sa + kk * 32), smem_desc_sw128(sa + kATileBytes + kk * 32), kIdesc,
-                   kb != kb0 || kk != 0 ? 1u : 0u);
-        umma_commit(&empty_bar[stage]);
-        if (++stage == S::kStages) { stage = 0; phase ^= 1u; }
-      }
-      ok = ok && mbar_wait(&count_bar, 0);
-      const uint32_t cnt = ok ? slices : 0;
-      for (uint32_t c = 0; c < cnt; ++c) {
-        const uint32_t slot = c % kLoraRing;
-        if (!mbar_wait_cl(&ls.full[slot], (c / kLoraRing) & 1u)) { ok = false; break; }
-        tc_fence_after();
-        const uint32_t sb = smem_u32(ext + slot * S::kBuf);
-        umma_f16(tmem_base, smem_desc_k32(sb), smem_desc_k32(sb + 128 * 32), kIdesc, 1u);
-        umma_commit(&ls.empty[slot]);
-      }
-      if (ok) umma_commit(&tfull_bar);
+  for (int i = 0; i < 2; ++i) xr[i] = s.tok[lr + i * 32] >= 0 ? p.x + s.tok[lr + i * 32] * p.ldx : nullptr;
+  const int fit = NC / p.rp;             // adapters of a pass
+  int pass = 0;
+  for (int l0 = blockIdx.y * fit; l0 < n_ad; l0 += fit * gridDim.y, ++pass) {
+    if (threadIdx.x < NJ) {
+      const int a = 8 * threadIdx.x / p.rp, l = l0 + a;
+      s_col[threadIdx.x] = a < fit && l < n_ad ? s.list[l] : -1;
+      s_r[threadIdx.x] = 8 * threadIdx.x - a * p.rp;
     }
-    __syncwarp();
-  } else {
-    // the adapters' slices of this rank
-    const int e = threadIdx.x - 64;
-    const int i0 = e < BN ? lora_id(a.ids, a.T, a.n, n0 + e) : -1;
-    const int nl = lora_list<128>(ls, e, i0, -1);
-    const int total = nl * (a.rp >> 4);
-    if (e == 0) {
-      slices = total > kr ? (total - kr - 1) / ks + 1 : 0;
-      mbar_arrive(&count_bar);
+    __syncthreads();
+    const int cols = min(fit, n_ad - l0) * p.rp;
+    const uint16_t* ar[(NC + 31) / 32];
+#pragma unroll
+    for (int i = 0; i < (NC + 31) / 32; ++i) {
+      const int row = lr + i * 32, id = s_col[row >> 3], r = s_r[row >> 3] + (row & 7);
+      ar[i] = id >= 0 && r < p.rank ? p.a_pool + (static_cast<size_t>(id) * p.rank + r) * p.K : nullptr;
     }
-    pdl_wait();
-    pdl_trigger();
-    LoraRing ring;
-    auto send = [&](uint32_t slot, bool, bool bad) {
-      if (bad)      // every rank's epilogue looks at its own flag
-        for (int r = 0; r < ks; ++r)
-          asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(mapa_rank(smem_u32(&ls.poison[0]), r)), "r"(kLoraPoison)
-                       : "memory");
-      mbar_arrive(&ls.full[slot]);
+    auto load = [&](int kb) {
+      const uint32_t st = ring + static_cast<uint32_t>((kb - kb0) % kStages) * (2 * S::kHalf);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int k = kb * 128 + h * 64 + lc * 8;
+        const uint32_t sh = st + h * S::kHalf;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int row = lr + i * 32;
+          const bool in = xr[i] && k < p.K;
+          cp_async16(sh + row * 128 + ((lc ^ (row & 7)) << 4), in ? xr[i] + k : p.x, in);
+        }
+#pragma unroll
+        for (int i = 0; i < (NC + 31) / 32; ++i) {
+          const int row = lr + i * 32;
+          const bool in = ar[i] && k < p.K;
+          if (row < cols) cp_async16(sh + (MT + row) * 128 + ((lc ^ (row & 7)) << 4), in ? ar[i] + k : p.a_pool, in);
+        }
+      }
     };
-    bool ok = lora_feed<BN, 128>(a, ls, ring, ext, 128 * 32, 0, S::kBuf, e, nl, kr, ks, n0 + e, i0, w0, send);
-    // the partial sums: lane = output, TMEM column = token
-    const int q = warp % 4, er = q * 32 + lane;
-    ok = ok && mbar_wait(&tfull_bar, 0);
-    if (__all_sync(0xffffffffu, ok)) {
-      tc_fence_after();
-      const uint32_t tb = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
-      const int ncmax = (BN + ks - 1) / ks;
-#pragma unroll 1
-      for (int c0 = 0; c0 < BN && n0 + c0 < a.T; c0 += 16) {
-        float f[16];
-        tmem_ld16(tb + c0, f);
-        tmem_ld_wait();
-        if (ks == 1) {
-          const bool poison = *reinterpret_cast<volatile uint32_t*>(&ls.poison[0]) != 0;
 #pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            const int t = n0 + c0 + j;
-            if (t < a.T && w0 + er < a.d_out) {
-              if (poison) f[j] += lora_nonfinite_term(a, t, w0 + er);
-              const __nv_bfloat16 b = __float2bfloat16_rn(f[j]);
-              y[t * ldy + w0 + er] = *reinterpret_cast<const uint16_t*>(&b);
-            }
-          }
-        } else {
+    for (int i = 0; i < kStages - 1; ++i) {
+      if (kb0 + i < kb1) load(kb0 + i);
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+    float acc[NJ][4] = {};
+    for (int kb = kb0; kb < kb1; ++kb) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+      __syncthreads();                   // stage kb has landed; stage kb - 1 is no longer read
+      if (kb + kStages - 1 < kb1) load(kb + kStages - 1);
+      asm volatile("cp.async.commit_group;" ::: "memory");
+      const uint32_t sh = ring + static_cast<uint32_t>((kb - kb0) % kStages) * (2 * S::kHalf) + wk * S::kHalf;
+      const int arow = wm * 16 + (lane & 15), hi = lane >> 4;
+      uint32_t a[4][4];
 #pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            const int c = c0 + j, s = ((c + 1) * ks - 1) / BN;       // the rank that owns column c
-            float* at = red + (kr * ncmax + c - s * BN / ks) * 128 + er;
-            asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(mapa_rank(smem_u32(at), s)), "f"(f[j]) : "memory");
+      for (int k = 0; k < 4; ++k) ldmatrix_x4(sh + arow * 128 + (((2 * k + hi) ^ (arow & 7)) << 4), a[k]);
+#pragma unroll
+      for (int j = 0; j < NJ; j += 2) {
+        if (j * 8 < cols) {
+          // rows j * 8 .. j * 8 + 15: matrices (rows 0-7, depth 0-7), (8-15, 0-7), (0-7, 8-15), (8-15, 8-15)
+          const int brow = j * 8 + (lane & 15);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            uint32_t b[4];
+            ldmatrix_x4(sh + (MT + brow) * 128 + (((2 * k + hi) ^ (brow & 7)) << 4), b);
+            mma_bf16_16816(acc[j], a[k][0], a[k][1], a[k][2], a[k][3], b[0], b[2]);
+            mma_bf16_16816(acc[j + 1], a[k][0], a[k][1], a[k][2], a[k][3], b[1], b[3]);
           }
         }
       }
     }
-  }
-  tc_fence_before();
-  __syncwarp();
-  if (ks > 1) cluster_sync_all();       // all partial sums and flags are in place
-  else __syncthreads();
-  tc_fence_after();
-  if (warp == 1) tmem_dealloc(tmem_base, S::kTmemCols);
-  if (ks > 1 && warp >= 2) {
-    const int er = (warp % 4) * 32 + lane;
-    const int ncmax = (BN + ks - 1) / ks;
-    const int lo = kr * BN / ks, hi = (kr + 1) * BN / ks;
-    const bool poison = ls.poison[0] != 0;
-    for (int c = lo; c < hi && n0 + c < a.T; ++c) {
-      float s = 0.f;
-      for (int r = 0; r < ks; ++r) s += red[(r * ncmax + c - lo) * 128 + er];
-      if (w0 + er < a.d_out) {
-        if (poison) s += lora_nonfinite_term(a, n0 + c, w0 + er);
-        const __nv_bfloat16 b = __float2bfloat16_rn(s);
-        y[(n0 + c) * ldy + w0 + er] = *reinterpret_cast<const uint16_t*>(&b);
-      }
-    }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    __syncthreads();
+    const int g = lane >> 2, tq = lane & 3;
+#pragma unroll
+    for (int j = 0; j < NJ; ++j)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        *reinterpret_cast<float2*>(&red[wk * kOut + (wm * 16 + h * 8 + g) * NC + j * 8 + 2 * tq]) =
+            make_float2(acc[j][2 * h], acc[j][2 * h + 1]);
+    __syncthreads();
+    auto halves = [&](int at, float* f) {
+      const float4* u = reinterpret_cast<const float4*>(red + at);
+      const float4* v = reinterpret_cast<const float4*>(red + kOut + at);
+      const float4 a = u[0], b = u[1], c = v[0], d = v[1];
+      f[0] = a.x + c.x; f[1] = a.y + c.y; f[2] = a.z + c.z; f[3] = a.w + c.w;
+      f[4] = b.x + d.x; f[5] = b.y + d.y; f[6] = b.z + d.z; f[7] = b.w + d.w;
+    };
+    shrink_store<MT, NC>(p, s, part + (pass & 1) * S::kPart, ks, kr, halves, [&](int c, int& r) {
+      r = s_r[c >> 3];
+      return s_col[c >> 3];
+    });
+    if (ks > 1) __syncthreads();         // the list of columns is free again
   }
 }
 
 // ---------------------------------------------------------------------------
 // Host side
 // ---------------------------------------------------------------------------
-template <int MI, int KS>
-static cudaError_t launch_shrink(const LoraCall& c, int rp, int split, cudaStream_t st) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(KS * ((c.T + 16 * MI - 1) / (16 * MI)), split);
-  cfg.blockDim = dim3(kShrinkWarps * 32);
-  cfg.stream = st;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = KS;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  return count_launch(cudaLaunchKernelEx(&cfg, lora_shrink_kernel<MI, KS>, c.x, c.ldx, c.T, c.d_in, c.a, c.scale, c.ids,
-                                         c.n, c.rank, rp, c.v));
-}
-
-template <int BN>
-static cudaError_t launch_proj(const LoraCall& c, const CUtensorMap& mW, const CUtensorMap& mX, const LoraArgs& la,
-                               cudaStream_t st) {
-  using S = ProjShape<BN>;
-  const int KB = (c.d_in + 63) / 64;
-  const int mt = (c.d_out + 127) / 128, nt = (c.T + BN - 1) / BN;
-  int ks = num_sms() / (mt * nt);
-  ks = ks < 1 ? 1 : ks > 8 ? 8 : ks;
-  if (ks > KB) ks = KB;
-  auto kern = lora_proj_kernel<BN>;
-  const size_t smem = S::smem(ks);
-  cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+// clusters: of ks blocks, that run at once; what the tiles leave of them shares out a tile's adapters.
+template <typename S>
+static cudaError_t launch_shrink(void (*kern)(ShrinkArgs), const ShrinkArgs& p, int ks, int clusters, cudaStream_t st) {
+  cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(S::kSmem));
   if (err != cudaSuccess) return err;
+  const int tiles = (p.T + S::MT - 1) / S::MT;
+  int split = clusters / tiles;
+  split = split < 1 ? 1 : split > 16 ? 16 : split;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ks, nt, mt);
-  cfg.blockDim = dim3(192);
-  cfg.dynamicSmemBytes = smem;
+  cfg.gridDim = dim3(ks * tiles, split);
+  cfg.blockDim = dim3(kShrinkThreads);
+  cfg.dynamicSmemBytes = S::kSmem;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -371,51 +433,42 @@ static cudaError_t launch_proj(const LoraCall& c, const CUtensorMap& mW, const C
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return count_launch(cudaLaunchKernelEx(&cfg, kern, mW, mX, la, c.d_in, c.y, c.ldy));
+  return count_launch(cudaLaunchKernelEx(&cfg, kern, p));
+}
+
+// Few tokens (a window): K over 8 or 4 blocks (two blocks per SM: 30 clusters of
+// 8, 66 of 4 at once).  Many: K split only as far as the tiles leave SMs idle
+// (one block per SM: 15 clusters of 8, 33 of 4, 74 of 2).
+static cudaError_t launch_shrink_for(const ShrinkArgs& p, cudaStream_t st) {
+  if (p.T <= kShrinkWindow) {
+    const int ks = p.T <= 64 ? 8 : 4, clusters = p.T <= 64 ? 28 : 64;
+    return p.rp <= 16   ? launch_shrink<ShrinkFew<2>>(lora_shrink_few_kernel<2>, p, ks, clusters, st)
+           : p.rp <= 32 ? launch_shrink<ShrinkFew<4>>(lora_shrink_few_kernel<4>, p, ks, clusters, st)
+                        : launch_shrink<ShrinkFew<8>>(lora_shrink_few_kernel<8>, p, ks, clusters / 2, st);
+  }
+  const int tiles = (p.T + 63) / 64;
+  const int ks = tiles <= 15 ? 8 : tiles <= 33 ? 4 : tiles <= 74 ? 2 : 1;
+  const int clusters = ks == 8 ? 15 : ks == 4 ? 33 : ks == 2 ? 74 : 148;
+  return p.rp <= 32 ? launch_shrink<ShrinkMany<8>>(lora_shrink_many_kernel<8>, p, ks, clusters, st)
+                    : launch_shrink<ShrinkMany<16>>(lora_shrink_many_kernel<16>, p, ks, clusters, st);
 }
 
 // Returns a message on failure, nullptr on success.
 const char* launch_lora(const LoraCall& c, cudaStream_t st, cudaError_t* cerr) {
   const int rp = (c.rank + 15) / 16 * 16;
-  EncodeTiledFn enc = get_encode_fn();
-  if (!enc) return "cuTensorMapEncodeTiled not found";
-  // v first
-  const int tiles16 = (c.T + 15) / 16;
-  if (c.T <= 512) {
-    int split = 600 / (tiles16 * 4);
-    split = split < 1 ? 1 : split > 16 ? 16 : split;
-    *cerr = launch_shrink<1, 4>(c, rp, split, st);
-  } else {
-    const int tiles = (c.T + 31) / 32;
-    int split = 600 / tiles;
-    split = split < 1 ? 1 : split > 16 ? 16 : split;
-    *cerr = launch_shrink<2, 1>(c, rp, split, st);
-  }
-  if (*cerr != cudaSuccess) return "adapter shrink launch failed";
-
+  *cerr = cudaSuccess;
   const int BNp = 256;     // the pair engine's column tile
   const long pair_tiles = static_cast<long>((c.T + 255) / 256) * ((c.d_out + BNp - 1) / BNp);
   const bool pairs = pair_tiles >= num_sms() / 4;
-  const uint32_t b_rows = pairs ? BNp / 2 : 128;
-  LoraArgs la;
-  {
-    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(c.rank), static_cast<cuuint64_t>(c.d_out), static_cast<cuuint64_t>(c.n)};
-    const cuuint64_t strides[2] = {2ull * c.rank, 2ull * c.rank * c.d_out};
-    const cuuint32_t box[3] = {16, b_rows, 1}, es[3] = {1, 1, 1};
-    if (enc(&la.b, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<uint16_t*>(c.b), dims, strides, box, es,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_32B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-      return "cuTensorMapEncodeTiled of the adapters failed";
-  }
-  la.ids = c.ids;
-  la.v = c.v;
-  la.b_pool = c.b;
-  la.T = c.T;
-  la.n = c.n;
-  la.rank = c.rank;
-  la.rp = rp;
-  la.d_out = c.d_out;
 
+  // v first
+  const size_t wb = 2ull * c.d_in * c.d_out;
+  const ShrinkArgs p = {c.x, c.ldx, c.T, c.d_in, c.a, c.scale, c.ids, c.n, c.rank, rp, c.v,
+                        reinterpret_cast<const uint8_t*>(c.w), !pairs && wb <= kPrefetchBytes ? wb : 0};
+  *cerr = launch_shrink_for(p, st);
+  if (*cerr != cudaSuccess) return "adapter shrink launch failed";
+
+  const LoraArgs la = {c.ids, c.v, c.b, c.T, c.n, c.rank, rp, c.d_out};
   if (pairs) {
     DenseArgs g = {};
     g.n = 1;
@@ -429,17 +482,15 @@ const char* launch_lora(const LoraCall& c, cudaStream_t st, cudaError_t* cerr) {
     *cerr = launch_dense<kEpiStore, 256, true>(g, st);
     return *cerr == cudaSuccess ? nullptr : "projection launch failed";
   }
-  const int bn = c.T <= 16 ? 16 : c.T <= 32 ? 32 : c.T <= 64 ? 64 : 128;
-  CUtensorMap mW, mX;
-  if (!dense_operand_map(&mW, c.w, false, c.d_out, c.d_in, 2ull * c.d_in, 128) ||
-      !dense_operand_map(&mX, c.x, false, c.T, c.d_in, 2ull * c.ldx, bn))
-    return "cuTensorMapEncodeTiled failed";
-  switch (bn) {
-    case 16: *cerr = launch_proj<16>(c, mW, mX, la, st); break;
-    case 32: *cerr = launch_proj<32>(c, mW, mX, la, st); break;
-    case 64: *cerr = launch_proj<64>(c, mW, mX, la, st); break;
-    default: *cerr = launch_proj<128>(c, mW, mX, la, st); break;
-  }
+  ProjArgs g = {};
+  g.T = c.T;
+  g.M = c.d_out;
+  g.early = 1;
+  g.out = c.y;
+  g.ld = c.ldy;
+  g.lora = la;
+  if (!proj_maps(g, c.w, false, c.d_out, c.d_in, 2ull * c.d_in, c.x, 2ull * c.ldx)) return "cuTensorMapEncodeTiled failed";
+  *cerr = launch_proj<kEpiStore, true>(g, st);
   return *cerr == cudaSuccess ? nullptr : "projection launch failed";
 }
 

@@ -7,8 +7,8 @@
 // v = s (x A[a]^T) of that adapter's tokens and zeros for all others, added in
 // the same accumulator.  So a tile may mix any requests, nothing is sorted, W
 // is read once, and B[a] is read by the tiles that hold one of its tokens.  The
-// extra range is fed in slices of 16 (one MMA deep): slices of v are written to
-// shared memory by threads, slices of B[a] come by TMA.
+// extra range is fed in slices of 16 (one MMA deep), a few to a message, which
+// four warps write to shared memory.
 //
 // A zero row does not mask an infinity or NaN of another request's adapter
 // (0 * inf = NaN).  The feeding threads see every slice of B[a], so they take
@@ -20,11 +20,11 @@
 
 namespace ftm {
 
-constexpr int kLoraRing = 4;              // slices in flight
-constexpr uint32_t kLoraData = 1, kLoraLast = 2, kLoraPoison = 4;
+constexpr int kLoraRing = 2;              // messages (groups of slices) in flight
+// a message: slices in it (low bits, 0: none), and
+constexpr uint32_t kLoraCount = 7, kLoraLast = 8, kLoraPoison = 16;
 
 struct LoraArgs {
-  CUtensorMap b;             // B pool: dims {rank, d_out, adapters}, box {16, rows of a slice}, 32-byte swizzle
   const int32_t* ids;        // [T] adapter of each token, -1: none
   const uint16_t* v;         // [T][rp] bf16, s (x A^T); rows of tokens without an adapter are never read
   const uint16_t* b_pool;    // [adapters][d_out][rank]
@@ -95,8 +95,8 @@ struct LoraShared {};
 
 template <>
 struct LoraShared<true> {
-  uint64_t full[kLoraRing], empty[kLoraRing], landed[kLoraRing];
-  uint32_t msg[kLoraRing];        // kLoraData | kLoraLast | kLoraPoison of the slice (even CTA)
+  uint64_t full[kLoraRing], empty[kLoraRing];
+  uint32_t msg[kLoraRing];        // the message (even CTA)
   uint32_t msg_peer[kLoraRing];   // the odd CTA's kLoraPoison
   uint32_t bad[kLoraRing];
   uint32_t poison[2];
@@ -104,12 +104,11 @@ struct LoraShared<true> {
   alignas(16) int32_t id[256];    // read 16 bytes at a time
   uint8_t list[256];              // rows at which an adapter occurs first
 
-  // full: one arrival of each CTA's feed (`ctas`); landed: the TMA's bytes
+  // full: one arrival of each CTA's feed
   __device__ __forceinline__ void init(int ctas = 2) {
     for (int s = 0; s < kLoraRing; ++s) {
       mbar_init(&full[s], ctas);
       mbar_init(&empty[s], 1);
-      mbar_init(&landed[s], 1);
       msg_peer[s] = 0;
       bad[s] = 0;
     }
@@ -120,104 +119,153 @@ struct LoraShared<true> {
 // Lists the distinct adapters of `ROWS` (128 or 256) tile rows in the order of
 // their first row: ls.id and ls.list are set, the count is returned.  Called by
 // the 128 feeding threads; e = thread.  i0 / i1: the ids of rows e and e + 128.
+// at: the list position of row e + 128 * which (meaningless for id -1).
 template <int ROWS>
-__device__ __forceinline__ int lora_list(LoraShared<true>& ls, int e, int i0, int i1) {
+__device__ __forceinline__ int lora_list(LoraShared<true>& ls, int e, int i0, int i1, int which, int& at) {
   feed_bar();                     // the previous tile's list is no longer read
   ls.id[e] = i0;
   if (ROWS == 256) ls.id[e + 128] = i1;
   feed_bar();
   const int w = e >> 5, lane = e & 31;
+  int first = 0;                  // first row with the id of row e + 128 * which
 #pragma unroll
   for (int half = 0; half < ROWS / 128; ++half) {
     const int id = half ? i1 : i0;
     const int wrow = half * 128 + w * 32;              // first row of this warp's 32
-    bool head = (__ffs(__match_any_sync(0xffffffffu, id)) - 1) == lane && id >= 0;
-    if (head)
-      for (int j = 0; j < wrow && head; j += 4) {
+    const int wfirst = __ffs(__match_any_sync(0xffffffffu, id)) - 1;
+    int at_row = wrow + wfirst;
+    if (wfirst == lane && id >= 0) {
+      for (int j = 0; j < wrow; j += 4) {
         const int4 o = *reinterpret_cast<const int4*>(&ls.id[j]);
-        head = o.x != id && o.y != id && o.z != id && o.w != id;
+        if (o.x == id || o.y == id || o.z == id || o.w == id) {
+          at_row = o.x == id ? j : o.y == id ? j + 1 : o.z == id ? j + 2 : j + 3;
+          break;
+        }
       }
-    const uint32_t m = __ballot_sync(0xffffffffu, head);
+    }
+    __syncwarp();
+    const uint32_t m = __ballot_sync(0xffffffffu, id >= 0 && at_row == wrow + lane);
     if (lane == 0) ls.heads[half * 4 + w] = m;
+    at_row = __shfl_sync(0xffffffffu, at_row, wfirst);
+    if (half == which) first = at_row;
   }
   feed_bar();
   int n = 0;
+  at = 0;
 #pragma unroll
   for (int k = 0; k < ROWS / 32; ++k) {
     const uint32_t m = ls.heads[k];
     if ((k & 3) == w && (m >> lane & 1u)) ls.list[n + __popc(m & ((1u << lane) - 1u))] = static_cast<uint8_t>(k * 32 + lane);
+    if (first >> 5 == k) at = n + __popc(m & ((1u << (first & 31)) - 1u));
     n += __popc(m);
   }
   feed_bar();
   return n;
 }
 
-// Position in the ring of slice buffers.
+// Position in the ring of message buffers.
 struct LoraRing {
-  uint32_t count = 0;             // slices passed so far
+  uint32_t count = 0;             // messages passed so far
 };
 
-// Feeds one tile's slices: those with index j = first, first + stride, ... of
-// the list's adapters x rank / 16.  Row `e` of the v slice is token `tok` when
-// e < NV (its adapter `mine`); the slice of B holds NB rows from output row n0.
-// v_at / b_at: byte offsets of the two operands in a ring buffer.  `send` hands
-// a finished slice on: send(slot, last, poison), by thread 0.
-template <int NV, int NB, typename Send>
+// Feeds one tile's slices: those with index first, first + stride, ... of the
+// list's adapters x rank / 16, G to a message, so that one round of barriers
+// serves G MMAs.  Row `e` of a v slice is token `tok` when e < NV (`mine`: its
+// adapter's list position, -1 for none); row e of a slice of B is output
+// n0 + e when e < NB.  A slice takes buf_bytes of the message's buffer, the
+// operands at v_at and b_at.  `ready()` is called before v is first read,
+// `send(slot, slices, last, poison)` by thread 0 for a finished message.  Each
+// thread moves its rows of both operands through registers, loaded one message
+// ahead: TMA boxes of 32-byte rows took 2 us a message, this takes 0.6.
+template <int NV, int NB, int G, typename Ready, typename Send>
 __device__ __forceinline__ bool lora_feed(const LoraArgs& a, LoraShared<true>& ls, LoraRing& ring, uint8_t* ext,
                                           uint32_t v_at, uint32_t b_at, uint32_t buf_bytes, int e, int n_list,
-                                          int first, int stride, int tok, int mine, int n0, Send send) {
+                                          int first, int stride, int tok, int mine, int n0, Ready ready, Send send) {
   const int per = a.rp >> 4;
   const int total = n_list * per;
   const int cnt = total > first ? (total - first - 1) / stride + 1 : 0;
-  const uint32_t base = ring.count;
-  auto issue = [&](int j) -> bool {        // thread 0: the slice of B into its buffer
-    const uint32_t c = base + j, slot = c % kLoraRing;
-    if (!mbar_wait_cl(&ls.empty[slot], ((c / kLoraRing) & 1u) ^ 1u)) return false;
-    const int sl = first + j * stride, li = sl / per;
-    mbar_arrive_expect_tx(&ls.landed[slot], NB * 32);
-    tma_load_3d(ext + slot * buf_bytes + b_at, &a.b, &ls.landed[slot], (sl - li * per) * 16, n0, ls.id[ls.list[li]]);
-    return true;
-  };
-  bool ok = true;
-  if (e == 0)
-    for (int j = 0; j < 2 && j < cnt && ok; ++j) ok = issue(j);
+  const int msgs = (cnt + G - 1) / G;
+  const uint4 zero = make_uint4(0, 0, 0, 0);
   const uint4* vrow = reinterpret_cast<const uint4*>(a.v + static_cast<size_t>(tok) * a.rp);
-  for (int j = 0; j < cnt; ++j) {
-    const uint32_t c = base + j, slot = c % kLoraRing, phase = (c / kLoraRing) & 1u;
-    const int sl = first + j * stride, li = sl / per, k = sl - li * per;
-    const int id = ls.id[ls.list[li]];
-    uint4 v0 = make_uint4(0, 0, 0, 0), v1 = v0;
-    if (e < NV && mine == id) { v0 = vrow[2 * k]; v1 = vrow[2 * k + 1]; }
-    if (e == 0 && ok && j + 2 < cnt) ok = issue(j + 2);
-    ok = ok && mbar_wait_cl(&ls.empty[slot], phase ^ 1u);
-    uint8_t* buf = ext + slot * buf_bytes;
-    if (ok && e < NV) {
-      const int sw = (e >> 2) & 1;
-      *reinterpret_cast<uint4*>(buf + v_at + e * 32 + sw * 16) = v0;
-      *reinterpret_cast<uint4*>(buf + v_at + e * 32 + (sw ^ 1) * 16) = v1;
+  const bool has_b = e < NB && n0 + e < a.d_out;
+  const uint16_t* brow = a.b_pool + (static_cast<size_t>(n0) + e) * a.rank;
+  const size_t b_pitch = static_cast<size_t>(a.d_out) * a.rank;      // between adapters
+  uint4 v[G][2], b[G][2];
+  int left = cnt, li = first / per, k = first - li * per;           // the next slice to load
+  auto load_b = [&](int s, int l, int kk) {
+    b[s][0] = b[s][1] = zero;
+    if (has_b) {
+      const uint4* p = reinterpret_cast<const uint4*>(brow + ls.id[ls.list[l]] * b_pitch + kk * 16);
+      b[s][0] = __ldg(p);
+      if (kk * 16 + 8 < a.rank) b[s][1] = __ldg(p + 1);
     }
-    ok = ok && mbar_wait_cl(&ls.landed[slot], phase);
-    if (ok && e < NB) {
-      // both halves of the row: their places do not matter for the check
-      uint4* p = reinterpret_cast<uint4*>(buf + b_at + e * 32);
+  };
+  auto load_v = [&](int s, int l, int kk) {
+    const bool use = e < NV && mine == l;
+    v[s][0] = use ? vrow[2 * kk] : zero;
+    v[s][1] = use ? vrow[2 * kk + 1] : zero;
+  };
+  // the next message's slices into registers; mask: 1 the rows of B, 2 those of v
+  auto load = [&](int mask, bool advance) {
+    int l = li, kk = k, n = left;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint4 w = p[h];
-        if (bf16_pair_nonfinite(w.x) || bf16_pair_nonfinite(w.y) || bf16_pair_nonfinite(w.z) || bf16_pair_nonfinite(w.w)) {
-          p[h] = make_uint4(bf16_pair_finite(w.x), bf16_pair_finite(w.y), bf16_pair_finite(w.z), bf16_pair_finite(w.w));
-          ls.bad[slot] = 1;
+    for (int s = 0; s < G; ++s) {
+      if (n > 0) {
+        if (mask & 1) load_b(s, l, kk);
+        if (mask & 2) load_v(s, l, kk);
+        for (kk += stride; kk >= per; kk -= per) ++l;
+        --n;
+      }
+    }
+    if (advance) { li = l; k = kk; left = n; }
+  };
+  load(1, false);          // B does not depend on the shrink
+  ready();
+  load(2, true);
+  bool ok = true;
+  for (int m = 0; m < msgs; ++m) {
+    const uint32_t slot = ring.count % kLoraRing, phase = (ring.count / kLoraRing) & 1u;
+    ring.count += 1;
+    const int n = min(G, cnt - m * G);
+    ok = ok && mbar_wait_cl(&ls.empty[slot], phase ^ 1u);
+    uint8_t* buf = ext + slot * G * buf_bytes;
+    bool bad = false;
+    if (ok) {
+      const int sw = (e >> 2) & 1;
+#pragma unroll
+      for (int s = 0; s < G; ++s) {
+        if (s < n) {
+          if (e < NV) {
+            uint8_t* row = buf + s * buf_bytes + v_at + e * 32;
+            *reinterpret_cast<uint4*>(row + sw * 16) = v[s][0];
+            *reinterpret_cast<uint4*>(row + (sw ^ 1) * 16) = v[s][1];
+          }
+          if (e < NB) {
+            uint8_t* row = buf + s * buf_bytes + b_at + e * 32;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              uint4 w = b[s][h];
+              if (bf16_pair_nonfinite(w.x) || bf16_pair_nonfinite(w.y) || bf16_pair_nonfinite(w.z) ||
+                  bf16_pair_nonfinite(w.w)) {
+                w = make_uint4(bf16_pair_finite(w.x), bf16_pair_finite(w.y), bf16_pair_finite(w.z), bf16_pair_finite(w.w));
+                bad = true;
+              }
+              *reinterpret_cast<uint4*>(row + (sw ^ h) * 16) = w;
+            }
+          }
         }
       }
     }
+    if (bad) ls.bad[slot] = 1;
+    load(3, true);
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     if (!feed_all(ok)) return false;
     if (e == 0) {
-      const bool bad = ls.bad[slot] != 0;
+      const bool any = ls.bad[slot] != 0;
       ls.bad[slot] = 0;
-      send(slot, j + 1 == cnt, bad);
+      send(slot, static_cast<uint32_t>(n), m + 1 == msgs, any);
     }
   }
-  ring.count = base + cnt;
   return true;
 }
 

@@ -1,0 +1,358 @@
+// Dense bf16 projections of few tokens, bound by the bytes of the weights:
+// out[t][m] = sum_k A[m][k] X[t][k] with the weight rows on the MMA's M side
+// (128 per tile) and BN tokens on its N side, so one token streams full weight
+// tiles.  A cluster of ks CTAs splits each tile's K; the partial sums cross
+// shared memory once, 16 bytes a store (every rank sums the outputs it owns, in
+// rank order, so the result does not depend on timing), and the epilogue runs
+// from there on pieces of 2 outputs of 4 tokens: a warp covers 64 outputs, 128
+// bytes of a token's row.
+//
+//   kEpiStore  out = D
+//   kEpiGated  64 gate rows and the 64 up rows of the same outputs per tile:
+//              out = act(g) * u, and g, u kept on request
+//   kEpiDgate  D = dh: dg, du and h from the kept g and u (A read rows-innermost)
+//   LORA       kEpiStore over K and the adapters' K range (ftm_lora.cuh); the
+//              slices are shared out over the cluster's ranks like K
+//
+// Shared memory stays under half an SM's for BN <= 64, so that the next launch
+// of the chain may move in early and load its weights while this one drains.
+#pragma once
+#include <stdlib.h>
+
+#include "ftm_dense.cuh"
+
+namespace ftm {
+
+constexpr int kProjThreads = 192;   // warp 0 TMA, warp 1 MMA, warps 2-5 adapters' feed and accumulator drain
+
+struct ProjArgs {
+  CUtensorMap a, x;        // weights (boxes of 64 rows x 64 deep, either majorness), tokens {K, T}
+  int T, M, kb;            // tokens, outputs, 64-deep blocks
+  int a_mn;                // A stored rows-innermost
+  int up_row0;             // gated: first up row of A
+  int act, keep;
+  int early;               // the launch before is this library's own, of the same call: A may be read before it ends
+  uint16_t* out;           // [T][ld]
+  int64_t ld;
+  uint16_t* pre;           // gated: g, u [T][2M] when kept; dgate: read
+  uint16_t* h;             // dgate: [T][M] when kept
+  LoraArgs lora;
+};
+
+template <int BN, bool LORA>
+struct ProjShape {
+  static constexpr uint32_t kBBytes = ((BN * 128 + 1023) / 1024) * 1024;
+  static constexpr uint32_t kStage = kATileBytes + kBBytes;
+  static constexpr int kStages = BN == 16 ? 5 : BN == 32 ? 4 : 3;
+  static constexpr int kGroup = 4;                                     // adapter slices per message
+  static constexpr uint32_t kBuf = LORA ? 128 * 32 + BN * 32 : 0;      // a slice of B[a] and one of v
+  static constexpr uint32_t kRed = BN * 512 + 8 * 64;                  // partial sums of every rank, each rounded up
+  static constexpr uint32_t kTmemCols = BN < 32 ? 32 : BN;
+  static constexpr size_t kSmem = 1024 + static_cast<size_t>(kStages) * kStage + kLoraRing * kGroup * kBuf + kRed;
+};
+
+__device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+
+__device__ __forceinline__ void st_cluster_f32x4(uint32_t addr, const float* f) {
+  st_cluster_v4(addr, f[0], f[1], f[2], f[3]);
+}
+
+template <int EPI, int BN, bool LORA>
+__global__ void __launch_bounds__(kProjThreads, 1) proj_kernel(const __grid_constant__ ProjArgs a) {
+  using S = ProjShape<BN, LORA>;
+  constexpr uint32_t kIdesc = idesc_bf16_f32(128, BN);
+  constexpr int kRows = EPI == kEpiGated ? 64 : 128;      // outputs per tile
+  constexpr int kPairs = kRows / 2;                       // pieces (2 outputs, 4 tokens) of 4 tokens
+  constexpr int kParts = EPI == kEpiGated ? 2 : 1;        // gate and up values of a piece
+
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t full_bar[S::kStages], empty_bar[S::kStages], tfull_bar, count_bar;
+  __shared__ uint32_t tmem_holder, slices;
+  __shared__ LoraShared<LORA> ls;
+
+  const uint32_t smem_base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  uint8_t* smem = smem_raw + (smem_base - smem_u32(smem_raw));
+  uint8_t* ext = smem + static_cast<size_t>(S::kStages) * S::kStage;
+  uint8_t* red = ext + kLoraRing * S::kGroup * S::kBuf;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int ks = static_cast<int>(cluster_nranks()), kr = static_cast<int>(cluster_rank());
+  const int n0 = blockIdx.y * BN, w0 = blockIdx.z * kRows;
+  const int valid = min(BN, a.T - n0);
+  const int kb0 = kr * a.kb / ks, kb1 = (kr + 1) * a.kb / ks;
+  // pieces of the tile, `share` of them summed by each rank; a piece is 32 bytes: [output][token]
+  const int pieces = (valid + 3) / 4 * kPairs, share = (pieces + ks - 1) / ks;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S::kStages; ++s) { mbar_init(&full_bar[s], 1); mbar_init(&empty_bar[s], 1); }
+    mbar_init(&tfull_bar, 1);
+    mbar_init(&count_bar, 1);
+    if constexpr (LORA) ls.init(1);
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(&tmem_holder, S::kTmemCols);
+    tmem_relinquish();
+  }
+  if (warp == 0 && lane == 0) { tma_prefetch_desc(&a.a); tma_prefetch_desc(&a.x); }
+  tc_fence_before();
+  if (ks > 1) cluster_sync_all();       // every rank's shared memory may be written from here on
+  else __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = tmem_holder;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      auto load_a = [&](int kb, int stage) {
+        uint8_t* sa = smem + static_cast<size_t>(stage) * S::kStage;
+        const int r1 = EPI == kEpiGated ? a.up_row0 + w0 : w0 + 64;
+        if (a.a_mn) {
+          tma_load_2d(sa, &a.a, &full_bar[stage], w0, kb * 64);
+          tma_load_2d(sa + 8192, &a.a, &full_bar[stage], r1, kb * 64);
+        } else {
+          tma_load_2d(sa, &a.a, &full_bar[stage], kb * 64, w0);
+          tma_load_2d(sa + 8192, &a.a, &full_bar[stage], kb * 64, r1);
+        }
+      };
+      // The launch before waited for everything earlier before it let this one
+      // start, and does not write A: the first stages' weights need no wait.
+      // (LORA: nor does the shrink write x.)
+      int ahead = 0;
+      if (a.early)
+        for (; ahead < S::kStages && kb0 + ahead < kb1; ++ahead) {
+          mbar_arrive_expect_tx(&full_bar[ahead], kATileBytes + BN * 128);
+          load_a(kb0 + ahead, ahead);
+        }
+      if (!LORA) { pdl_wait(); pdl_trigger(); }
+      int stage = 0;
+      uint32_t phase = 0;
+      for (int kb = kb0; kb < kb1; ++kb) {
+        if (kb - kb0 >= ahead) {
+          if (!mbar_wait(&empty_bar[stage], phase ^ 1u)) break;
+          mbar_arrive_expect_tx(&full_bar[stage], kATileBytes + BN * 128);
+          load_a(kb, stage);
+        }
+        tma_load_2d(smem + static_cast<size_t>(stage) * S::kStage + kATileBytes, &a.x, &full_bar[stage], kb * 64, n0);
+        if (++stage == S::kStages) { stage = 0; phase ^= 1u; }
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (lane == 0) {
+      const bool amn = a.a_mn;
+      const uint32_t idesc = kIdesc | (amn ? 1u << 15 : 0u);
+      int stage = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int kb = kb0; kb < kb1; ++kb) {
+        if (!mbar_wait(&full_bar[stage], phase)) { ok = false; break; }
+        tc_fence_after();
+        const uint32_t sa = smem_u32(smem + static_cast<size_t>(stage) * S::kStage);
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+          umma_f16(tmem_base, amn ? smem_desc_mn_sw128(sa + kk * 2048) : smem_desc_sw128(sa + kk * 32),
+                   smem_desc_sw128(sa + kATileBytes + kk * 32), idesc, kb != kb0 || kk != 0 ? 1u : 0u);
+        umma_commit(&empty_bar[stage]);
+        if (++stage == S::kStages) { stage = 0; phase ^= 1u; }
+      }
+      if constexpr (LORA) {
+        ok = ok && mbar_wait(&count_bar, 0);
+        const uint32_t cnt = ok ? slices : 0;
+        for (uint32_t c = 0; c * S::kGroup < cnt; ++c) {
+          const uint32_t slot = c % kLoraRing;
+          if (!mbar_wait_cl(&ls.full[slot], (c / kLoraRing) & 1u)) { ok = false; break; }
+          tc_fence_after();
+          const uint32_t n = min(static_cast<uint32_t>(S::kGroup), cnt - c * S::kGroup);
+          for (uint32_t s = 0; s < n; ++s) {
+            const uint32_t sb = smem_u32(ext + (slot * S::kGroup + s) * S::kBuf);
+            umma_f16(tmem_base, smem_desc_k32(sb), smem_desc_k32(sb + 128 * 32), kIdesc, 1u);
+          }
+          umma_commit(&ls.empty[slot]);
+        }
+      }
+      if (ok) umma_commit(&tfull_bar);
+    }
+    __syncwarp();
+  } else {
+    bool ok = true;
+    if constexpr (LORA) {
+      const int e = threadIdx.x - 64;
+      const int i0 = e < BN ? lora_id(a.lora.ids, a.T, a.lora.n, n0 + e) : -1;
+      int at;
+      const int nl = lora_list<128>(ls, e, i0, -1, 0, at);
+      const int total = nl * (a.lora.rp >> 4);
+      if (e == 0) {
+        slices = total > kr ? (total - kr - 1) / ks + 1 : 0;
+        mbar_arrive(&count_bar);
+      }
+      LoraRing ring;
+      auto ready = [] { pdl_wait(); pdl_trigger(); };      // the shrink's v
+      auto send = [&](uint32_t slot, uint32_t, bool, bool bad) {
+        if (bad)      // every rank's epilogue looks at its own flag
+          for (int r = 0; r < ks; ++r)
+            asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(mapa_rank(smem_u32(&ls.poison[0]), r)), "r"(kLoraPoison)
+                         : "memory");
+        mbar_arrive(&ls.full[slot]);
+      };
+      ok = lora_feed<BN, 128, S::kGroup>(a.lora, ls, ring, ext, 128 * 32, 0, S::kBuf, e, nl, kr, ks, n0 + e,
+                                         i0 >= 0 ? at : -1, w0, ready, send);
+    }
+    // this rank's partial sums to the ranks that own them: lane = weight row, TMEM column = token
+    const int q = warp % 4, er = q * 32 + lane;
+    ok = ok && mbar_wait(&tfull_bar, 0);
+    if (__all_sync(0xffffffffu, ok)) {
+      tc_fence_after();
+      const uint32_t tb = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
+      // piece (tokens 4 g .. 4 g + 3, outputs of this row's pair): its owner and its place there
+      const uint32_t mine = smem_u32(red) + (kr * kParts + er / kRows) * share * 32 + (er & 1) * 16;
+      int local = (er % kRows) / 2, owner = 0;
+#pragma unroll 1
+      for (int c0 = 0; c0 < valid; c0 += 16) {
+        float f[16];
+        tmem_ld16(tb + c0, f);
+        tmem_ld_wait();
+#pragma unroll
+        for (int j = 0; j < 16; j += 4) {
+          if (c0 + j < valid) {
+            while (local >= share) { local -= share; ++owner; }
+            st_cluster_f32x4(mapa_rank(mine + local * 32, owner), f + j);
+            local += kPairs;
+          }
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncwarp();
+  if (ks > 1) cluster_sync_all();       // all partial sums and flags are in place
+  else __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem_base, S::kTmemCols);
+
+  if (!LORA) pdl_wait();                // over since the loads began; every thread that reads `pre` asks for itself
+  bool poison = false;
+  if constexpr (LORA) poison = ls.poison[0] != 0;
+  for (int i = threadIdx.x; i < share; i += kProjThreads) {
+    const int piece = kr * share + i;
+    if (piece >= pieces) break;
+    const int t0 = n0 + piece / kPairs * 4, m = w0 + piece % kPairs * 2;
+    if (m >= a.M) continue;
+    auto sum = [&](int part, float* f) {       // f[output * 4 + token]
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f[j] = 0.f;
+      for (int r = 0; r < ks; ++r) {
+        const float4* p = reinterpret_cast<const float4*>(red + ((r * kParts + part) * share + i) * 32);
+        const float4 u = p[0], v = p[1];
+        f[0] += u.x; f[1] += u.y; f[2] += u.z; f[3] += u.w;
+        f[4] += v.x; f[5] += v.y; f[6] += v.z; f[7] += v.w;
+      }
+    };
+    float f[8], u[8];
+    sum(0, f);
+    if (EPI == kEpiGated) sum(1, u);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int t = t0 + j;
+      if (t >= a.T) break;
+      float v0 = f[j], v1 = f[4 + j];
+      uint16_t* o = a.out + t * a.ld + m;
+      uint16_t* p = a.pre + static_cast<size_t>(t) * (2 * static_cast<size_t>(a.M)) + m;
+      if constexpr (EPI == kEpiStore) {
+        if constexpr (LORA) {
+          if (poison) {
+            v0 += lora_nonfinite_term(a.lora, t, m);
+            v1 += lora_nonfinite_term(a.lora, t, m + 1);
+          }
+        }
+        *reinterpret_cast<uint32_t*>(o) = pack_bf16(v0, v1);
+      } else if constexpr (EPI == kEpiGated) {
+        const float u0 = u[j], u1 = u[4 + j];
+        *reinterpret_cast<uint32_t*>(o) = pack_bf16(act_value(v0, a.act) * u0, act_value(v1, a.act) * u1);
+        if (a.keep) {
+          *reinterpret_cast<uint32_t*>(p) = pack_bf16(v0, v1);
+          *reinterpret_cast<uint32_t*>(p + a.M) = pack_bf16(u0, u1);
+        }
+      } else {
+        const uint32_t gw = __ldg(reinterpret_cast<const uint32_t*>(p)), uw = __ldg(reinterpret_cast<const uint32_t*>(p + a.M));
+        float dg0, dg1, du0, du1, h0, h1;
+        act_gradient(__uint_as_float(gw << 16), __uint_as_float(uw << 16), v0, a.act, dg0, du0, h0);
+        act_gradient(__uint_as_float(gw & 0xffff0000u), __uint_as_float(uw & 0xffff0000u), v1, a.act, dg1, du1, h1);
+        *reinterpret_cast<uint32_t*>(o) = pack_bf16(dg0, dg1);
+        *reinterpret_cast<uint32_t*>(o + a.M) = pack_bf16(du0, du1);
+        if (a.keep) *reinterpret_cast<uint32_t*>(a.h + static_cast<size_t>(t) * a.M + m) = pack_bf16(h0, h1);
+      }
+    }
+  }
+}
+
+// ---- host ------------------------------------------------------------------------
+
+template <int EPI, int BN, bool LORA>
+cudaError_t launch_proj_bn(const ProjArgs& a, cudaStream_t st) {
+  using S = ProjShape<BN, LORA>;
+  const int mt = (a.M + (EPI == kEpiGated ? 63 : 127)) / (EPI == kEpiGated ? 64 : 128), nt = (a.T + BN - 1) / BN;
+  const long tiles = static_cast<long>(mt) * nt;
+  auto kern = proj_kernel<EPI, BN, LORA>;
+  cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(S::kSmem));
+  if (err != cudaSuccess) return err;
+  cudaLaunchConfig_t cfg = {};
+  cfg.blockDim = dim3(kProjThreads);
+  cfg.dynamicSmemBytes = S::kSmem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 1;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  // The widest split whose clusters all run at once: a second wave doubles the
+  // time, and clusters do not fill every GPC (15 of 8 CTAs on 148 SMs at one
+  // CTA per SM, which is what the query reports).
+  struct Fit { int n[9]; };
+  static const Fit fit = [&] {
+    Fit f = {};
+    for (int c = 2; c <= 8; ++c) {
+      attr[0].val.clusterDim.x = c;
+      cfg.gridDim = dim3(num_sms() / c * c);
+      if (cudaOccupancyMaxActiveClusters(&f.n[c], kern, &cfg) != cudaSuccess) f.n[c] = 0;
+    }
+    (void)cudaGetLastError();
+    return f;
+  }();
+  constexpr int kPerSm = 2 * (S::kSmem + 2048) <= 228 * 1024 ? 2 : 1;
+  int ks = 1;
+  for (int c = 2; c <= 8 && c <= a.kb && c * tiles <= num_sms(); ++c)
+    if (tiles <= kPerSm * fit.n[c]) ks = c;
+  cfg.gridDim = dim3(ks, nt, mt);
+  attr[0].val.clusterDim.x = ks;
+  cfg.numAttrs = 2;
+  return count_launch(cudaLaunchKernelEx(&cfg, kern, a));
+}
+
+// Token tile: the smallest that holds all tokens, 128 beyond.
+inline int proj_tile(int T) { return T <= 16 ? 16 : T <= 32 ? 32 : T <= 64 ? 64 : 128; }
+
+template <int EPI, bool LORA>
+cudaError_t launch_proj(const ProjArgs& a, cudaStream_t st) {
+  switch (proj_tile(a.T)) {
+    case 16: return launch_proj_bn<EPI, 16, LORA>(a, st);
+    case 32: return launch_proj_bn<EPI, 32, LORA>(a, st);
+    case 64: return launch_proj_bn<EPI, 64, LORA>(a, st);
+    default: return launch_proj_bn<EPI, 128, LORA>(a, st);
+  }
+}
+
+// Maps of the weights [M][K] (a_mn: stored [K][M], M innermost) and the tokens [T][K].
+inline bool proj_maps(ProjArgs& a, const void* w, bool a_mn, uint64_t w_rows, uint64_t K, uint64_t w_pitch,
+                      const void* x, uint64_t x_pitch) {
+  a.a_mn = a_mn;
+  a.kb = static_cast<int>((K + 63) / 64);
+  return dense_operand_map(&a.a, w, a_mn, w_rows, K, w_pitch, 64) &&
+         dense_operand_map(&a.x, x, false, a.T, K, x_pitch, proj_tile(a.T));
+}
+
+}  // namespace ftm
