@@ -21,10 +21,11 @@
 
 namespace ftm {
 
-// Whether an [M][N] product has too few of the pair engine's tiles to occupy the GPU.
-static bool few_tiles(int M, int N, int cols) {
-  return static_cast<long>((M + kDTileM - 1) / kDTileM) * ((N + cols - 1) / cols) < num_sms() / 4;
+// Tiles of an [M][N] product on the pair engine, and whether they are too few to occupy the GPU.
+static long pair_tiles(int M, int N, int cols) {
+  return static_cast<long>((M + kDTileM - 1) / kDTileM) * ((N + cols - 1) / cols);
 }
+static bool few_tiles(int M, int N, int cols) { return pair_tiles(M, N, cols) < num_sms() / 4; }
 
 const char* launch_gated_ffn(int act, const void* x, int T, int d, int I, const void* bank, size_t w_d_off, void* pre,
                              void* h, void* y, cudaStream_t st, cudaError_t* cerr) {
@@ -44,7 +45,7 @@ const char* launch_gated_ffn(int act, const void* x, int T, int d, int I, const 
     g.out = static_cast<uint16_t*>(h);
     g.ld = I;
     g.pre = static_cast<uint16_t*>(pre);
-    if (!proj_maps(g, w, false, 2ull * I, d, rd, x, rd)) return maps;
+    if (!proj_maps(g, w, false, 2ull * I, d, rd, x, false, rd)) return maps;
     *cerr = launch_proj<kEpiGated, false>(g, st);
   } else {
     DenseArgs g = {};
@@ -55,9 +56,9 @@ const char* launch_gated_ffn(int act, const void* x, int T, int d, int I, const 
     dense_tiles(P, T, I, d, 128);
     P.up_row0 = I;
     if (!dense_operand_map(&P.a, x, false, T, d, rd, 128) || !dense_operand_map(&P.b, w, false, 2ull * I, d, rd, 128) ||
-        !dense_store_map(&P.c0, h, I, T, rI))
+        !dense_half_map(&P.c0, h, I, T, rI))
       return maps;
-    if (pre && (!dense_store_map(&P.c1, pp, I, T, 2 * rI) || !dense_store_map(&P.c2, pp + rI, I, T, 2 * rI))) return maps;
+    if (pre && (!dense_half_map(&P.c1, pp, I, T, 2 * rI) || !dense_half_map(&P.c2, pp + rI, I, T, 2 * rI))) return maps;
     *cerr = launch_dense<kEpiGated, 256, false>(g, st);
   }
   prof_mark(FTM_K_GEMM1, st, true);
@@ -70,7 +71,7 @@ const char* launch_gated_ffn(int act, const void* x, int T, int d, int I, const 
     g.early = 1;
     g.out = static_cast<uint16_t*>(y);
     g.ld = d;
-    if (!proj_maps(g, w + w_d_off, false, d, I, rI, h, rI)) return maps;
+    if (!proj_maps(g, w + w_d_off, false, d, I, rI, h, false, rI)) return maps;
     *cerr = launch_proj<kEpiStore, false>(g, st);
   } else {
     DenseArgs g = {};
@@ -105,48 +106,75 @@ const char* launch_gated_ffn_backward(int act, const void* x, int T, int d, int 
     g.ld = 2ll * I;
     g.pre = static_cast<uint16_t*>(const_cast<void*>(pre));
     g.h = static_cast<uint16_t*>(h);
-    if (!proj_maps(g, w + w_d_off, true, I, d, rI, dy, rd)) return maps;
+    if (!proj_maps(g, w + w_d_off, true, I, d, rI, dy, false, rd)) return maps;
     *cerr = launch_proj<kEpiDgate, false>(g, st);
   } else {
     DenseArgs g = {};
     g.n = 1;
     g.act = act;
     g.keep = dw_d != nullptr;
-    g.pre = static_cast<const uint16_t*>(pre);
+    const uint8_t* pp = static_cast<const uint8_t*>(pre);
     DenseProblem& P = g.p[0];
     dense_tiles(P, T, I, d, 256);
     P.b_mn = 1;
     if (!dense_operand_map(&P.a, dy, false, T, d, rd, 128) || !dense_operand_map(&P.b, w + w_d_off, true, I, d, rI, 0) ||
-        !dense_store_map(&P.c0, dg, I, T, 2 * rI) || !dense_store_map(&P.c1, dg + rI, I, T, 2 * rI) ||
-        !dense_store_map(&P.c2, h, I, T, rI))
+        !dense_half_map(&P.c0, dg, I, T, 2 * rI) || !dense_half_map(&P.c1, dg + rI, I, T, 2 * rI) ||
+        !dense_half_map(&P.c2, h, I, T, rI) || !dense_half_map(&P.p0, pp, I, T, 2 * rI) ||
+        !dense_half_map(&P.p1, pp + rI, I, T, 2 * rI))
       return maps;
     *cerr = launch_dense<kEpiDgate, 256, false>(g, st);
   }
   if (*cerr != cudaSuccess) return "activation gradient launch failed";
+  // The products.  Each is out[rows][cols] = P Q^T over depth K; those too
+  // small for the pair engine's tiles, but deep, run split along K instead.
+  struct Product {
+    const void *p, *q;                 // [rows][K] and [cols][K], or stored [K][...] where mn
+    bool p_mn, q_mn;
+    int rows, cols, K;
+    uint64_t p_pitch, q_pitch;
+    void* out;
+  };
+  const Product all[3] = {
+      {dgu, x, true, true, 2 * I, d, T, 2 * rI, rd, dw_gu},      // dWgu = dgu^T x
+      {dy, h, true, true, d, I, T, rd, rI, dw_d},                // dWd = dy^T h
+      {dgu, w, false, true, T, d, 2 * I, 2 * rI, rd, dx},        // dx = dgu Wgu
+  };
+  const bool split_w = T >= 512 && pair_tiles(2 * I, d, 256) + pair_tiles(d, I, 256) < num_sms() / 4;
+  const bool split[3] = {split_w, split_w, 2 * I >= 512 && few_tiles(T, d, 256)};
   DenseArgs g = {};
-  bool ok = true;
-  if (dw_d) {
-    DenseProblem& Q = g.p[g.n++];        // dWgu [2I][d] = dgu^T x
-    dense_tiles(Q, 2 * I, d, T, 256);
-    Q.a_mn = Q.b_mn = 1;
-    ok = ok && dense_operand_map(&Q.a, dgu, true, 2ull * I, T, 2 * rI, 0) &&
-         dense_operand_map(&Q.b, x, true, d, T, rd, 0) && dense_store_map(&Q.c0, dw_gu, d, 2ull * I, rd);
-    DenseProblem& R = g.p[g.n++];        // dWd [d][I] = dy^T h
-    dense_tiles(R, d, I, T, 256);
-    R.a_mn = R.b_mn = 1;
-    ok = ok && dense_operand_map(&R.a, dy, true, d, T, rd, 0) && dense_operand_map(&R.b, h, true, I, T, rI, 0) &&
-         dense_store_map(&R.c0, dw_d, I, d, rI);
+  bool launched = false;
+  for (int i = 0; i < 3; ++i) {
+    const Product& P = all[i];
+    if (!P.out || split[i]) continue;
+    DenseProblem& Q = g.p[g.n++];
+    dense_tiles(Q, P.rows, P.cols, P.K, 256);
+    Q.a_mn = P.p_mn;
+    Q.b_mn = P.q_mn;
+    if (!dense_operand_map(&Q.a, P.p, P.p_mn, P.rows, P.K, P.p_pitch, 128) ||
+        !dense_operand_map(&Q.b, P.q, P.q_mn, P.cols, P.K, P.q_pitch, 0) ||
+        !dense_store_map(&Q.c0, P.out, P.cols, P.rows, 2ull * P.cols))
+      return maps;
   }
-  if (dx) {
-    DenseProblem& Q = g.p[g.n++];        // dx = dgu Wgu
-    dense_tiles(Q, T, d, 2 * I, 256);
-    Q.b_mn = 1;
-    ok = ok && dense_operand_map(&Q.a, dgu, false, T, 2ull * I, 2 * rI, 128) &&
-         dense_operand_map(&Q.b, w, true, d, 2ull * I, rd, 0) && dense_store_map(&Q.c0, dx, d, T, rd);
+  if (g.n) {
+    *cerr = launch_dense<kEpiStore, 256, false>(g, st);
+    if (*cerr != cudaSuccess) return "gradient products launch failed";
+    launched = true;
   }
-  if (!ok) return maps;
-  *cerr = launch_dense<kEpiStore, 256, false>(g, st);
-  return *cerr == cudaSuccess ? nullptr : "gradient products launch failed";
+  for (int i = 0; i < 3; ++i) {
+    const Product& P = all[i];
+    if (!P.out || !split[i]) continue;
+    ProjArgs s = {};
+    s.T = P.rows;
+    s.M = P.cols;
+    s.early = launched ? 2 : 0;        // the first waits for dg, du and h, those behind it for nothing but the end
+    s.out = static_cast<uint16_t*>(P.out);
+    s.ld = P.cols;
+    if (!proj_maps(s, P.q, P.q_mn, P.cols, P.K, P.q_pitch, P.p, P.p_mn, P.p_pitch)) return maps;
+    *cerr = launch_proj<kEpiStore, false>(s, st);
+    if (*cerr != cudaSuccess) return "gradient product launch failed";
+    launched = true;
+  }
+  return nullptr;
 }
 
 }  // namespace ftm

@@ -29,6 +29,7 @@ constexpr int kDTileM = 256;                   // rows per tile (128 per CTA)
 constexpr int kDBK = 64;                       // depth per stage
 constexpr uint32_t kDABytes = 128 * 128;       // 128 rows x 64 deep of bf16 per CTA
 constexpr int kDSlotBytes = 32 * 128;          // one warp's staging slot: 32 rows x 64 columns of bf16
+constexpr int kDHalfBytes = 32 * 64;           // the epilogues with several tensors: 32 rows x 32 columns each
 constexpr int kDProblems = 3;
 
 enum DenseEpi {
@@ -38,7 +39,7 @@ enum DenseEpi {
 };
 
 struct DenseProblem {
-  CUtensorMap a, b, c0, c1, c2;
+  CUtensorMap a, b, c0, c1, c2, p0, p1;      // operands, outputs; dgate: the kept g and u
   int M, N;          // rows, output columns (gated: columns of h)
   int nt;            // column tiles
   int kb;            // 64-deep blocks
@@ -52,7 +53,6 @@ struct DenseArgs {
   int n;             // problems, deepest first
   int act;           // ftm_act
   int keep;          // gated: store g and u; dgate: store h
-  const uint16_t* pre;   // dgate: kept g and u, [M][2N]
   // tile schedule (see dense_tile_at)
   int n_long, n_short, short_extra;
   LoraArgs lora;
@@ -99,6 +99,15 @@ __device__ __forceinline__ void stage_half(uint8_t* slot, int row, int half, con
   }
 }
 
+// One row's 32 columns in a half slot, whose maps swizzle over 64 bytes.
+__device__ __forceinline__ uint4* half_piece(uint8_t* slot, int row, int c) {
+  return reinterpret_cast<uint4*>(slot + row * 64 + ((c ^ ((row >> 1) & 3)) << 4));
+}
+__device__ __forceinline__ void stage_row(uint8_t* slot, int row, const uint32_t* w) {
+#pragma unroll
+  for (int c = 0; c < 4; ++c) *half_piece(slot, row, c) = make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+}
+
 // ---- tile schedule ---------------------------------------------------------------
 // The pair's i-th tile, or -1.  Tiles [0, n_long) have the deepest K and go
 // round the pairs first; a pair that got one fewer takes short_extra shallow
@@ -141,30 +150,39 @@ __device__ __forceinline__ DenseTile dense_decode(const DenseArgs& g, int t) {
   return d;
 }
 
-template <int BN, bool LORA>
+// Epilogue warps and their staging.  kEpiStore: four warps, two slots each in
+// turn.  The others, whose arithmetic takes as long as a shallow product's MMAs
+// (with four warps the activation gradient took 18 us a tile at 640 deep, a
+// product of 4 us), run eight, two to a quadrant of rows with every other chunk
+// of 32 columns: kEpiGated one set of three half slots (h, g, u); kEpiDgate two
+// sets in turn, into which g and u are loaded a chunk ahead and which dg, du and
+// h leave from.
+template <int EPI, int BN, bool LORA>
 struct DenseShape {
   static constexpr uint32_t kBBytes = BN / 2 * 128;
   static constexpr uint32_t kStage = kDABytes + kBBytes;
-  static constexpr int kSlots = LORA ? 2 : 3;                      // staging slots per epilogue warp
-  static constexpr uint32_t kStaging = 4 * kSlots * kDSlotBytes;
+  static constexpr int kEpiWarps = EPI == kEpiStore ? 4 : 8;
+  static constexpr uint32_t kWarpStaging = EPI == kEpiStore ? 2 * kDSlotBytes : (EPI == kEpiGated ? 3 : 6) * kDHalfBytes;
+  static constexpr uint32_t kStaging = kEpiWarps * kWarpStaging;
   static constexpr int kGroup = 2;                                 // adapter slices per message
   static constexpr uint32_t kBuf = 128 * 32 + BN / 2 * 32;         // a slice of v and one of B[a]
   static constexpr uint32_t kExt = LORA ? kLoraRing * kGroup * kBuf : 0;
-  static constexpr int kStages = BN == 256 ? 5 : LORA ? 6 : 7;
+  static constexpr int kStages = BN == 256 ? (EPI == kEpiDgate ? 4 : 5) : EPI == kEpiStore && !LORA ? 7 : 6;
   static constexpr size_t kSmem = 1024 + static_cast<size_t>(kStages) * kStage + kStaging + kExt;
-  static constexpr int kThreads = LORA ? 320 : 192;
+  static constexpr int kThreads = 64 + 32 * kEpiWarps + (LORA ? 128 : 0);
 };
 
 template <int EPI, int BN, bool LORA>
-__global__ void __launch_bounds__(DenseShape<BN, LORA>::kThreads, 1)
+__global__ void __launch_bounds__(DenseShape<EPI, BN, LORA>::kThreads, 1)
     dense_kernel(const __grid_constant__ DenseArgs g) {
-  using S = DenseShape<BN, LORA>;
+  using S = DenseShape<EPI, BN, LORA>;
   constexpr int kStages = S::kStages;
   constexpr uint32_t kTmemCols = 2 * BN;
   constexpr int kOutCols = EPI == kEpiGated ? BN / 2 : BN;   // output columns per tile
 
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t full_bar[kStages], empty_bar[kStages], tfull_bar[2], tempty_bar[2];
+  __shared__ __align__(8) uint64_t pre_bar[EPI == kEpiDgate ? 16 : 1];     // [warp][set]: g and u of a chunk
   __shared__ uint32_t tmem_holder;
   __shared__ LoraShared<LORA> ls;
 
@@ -179,7 +197,9 @@ __global__ void __launch_bounds__(DenseShape<BN, LORA>::kThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) { mbar_init(&full_bar[s], 1); mbar_init(&empty_bar[s], 1); }
-    for (int a = 0; a < 2; ++a) { mbar_init(&tfull_bar[a], LORA ? 2 : 1); mbar_init(&tempty_bar[a], 8); }
+    for (int a = 0; a < 2; ++a) { mbar_init(&tfull_bar[a], LORA ? 2 : 1); mbar_init(&tempty_bar[a], 2 * S::kEpiWarps); }
+    if (EPI == kEpiDgate)
+      for (int i = 0; i < 16; ++i) mbar_init(&pre_bar[i], 1);
     if constexpr (LORA) ls.init();
     fence_mbar_init();
   }
@@ -295,114 +315,135 @@ __global__ void __launch_bounds__(DenseShape<BN, LORA>::kThreads, 1)
       }
     }
     __syncwarp();
-  } else if (warp < 6) {
+  } else if (warp < 2 + S::kEpiWarps) {
     const int q = warp % 4;           // TMEM lane quadrant
     const uint32_t tempty0 = mapa_rank(smem_u32(&tempty_bar[0]), 0);
     const uint32_t tempty1 = mapa_rank(smem_u32(&tempty_bar[1]), 0);
-    uint8_t* slots = staging + (warp - 2) * S::kSlots * kDSlotBytes;
-    int chunk = 0;                    // chunks stored so far: kEpiStore alternates between two slots
+    uint8_t* slots = staging + (warp - 2) * S::kWarpStaging;
+    constexpr int kCols = EPI == kEpiStore ? 64 : 32;      // columns of a chunk
+    constexpr int kTurns = S::kEpiWarps / 4;               // warps that share a quadrant's chunks
+    const int first = (warp - 2) / 4;
+    uint32_t chunk = 0;               // chunks of this warp so far: slots and sets take turns
+    uint64_t* pbar = pre_bar + (EPI == kEpiDgate ? (warp - 2) * 2 : 0);
     for (int i = 0, t; (t = dense_tile_at(g, pair, np, i)) >= 0; ++i) {
       const DenseTile ti = dense_decode(g, t);
       const DenseProblem& P = g.p[ti.p];
       const int ab = i & 1;
-      if (!__all_sync(0xffffffffu, mbar_wait_cl(&tfull_bar[ab], (i >> 1) & 1))) break;
-      tc_fence_after();
       const int row0 = ti.m * kDTileM + static_cast<int>(rank) * 128 + q * 32;   // this warp's 32 rows
       const int row = row0 + lane;
       const int col0 = ti.n * kOutCols;
+      const int chunks = row0 < P.M ? (min(kOutCols, P.N - col0) + kCols - 1) / kCols : 0;
+      auto ask = [&](int c, uint32_t n) {      // lane 0: g and u of the tile's chunk c into the set of this warp's n-th
+        uint8_t* in = slots + (n & 1) * 3 * kDHalfBytes;
+        mbar_arrive_expect_tx(&pbar[n & 1], 2 * kDHalfBytes);
+        tma_load_2d(in, &P.p0, &pbar[n & 1], col0 + c * kCols, row0);
+        tma_load_2d(in + kDHalfBytes, &P.p1, &pbar[n & 1], col0 + c * kCols, row0);
+      };
+      if (EPI == kEpiDgate && lane == 0 && first < chunks) {
+        bulk_wait_read<0>();
+        ask(first, chunk);
+      }
+      bool ok = mbar_wait_cl(&tfull_bar[ab], (i >> 1) & 1);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      tc_fence_after();
       const uint32_t tb = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + ab * BN;
       bool poison = false;
       if constexpr (LORA) poison = ls.poison[ab] != 0;
-      if (row0 < P.M) {
 #pragma unroll 1
-        for (int c0 = 0; c0 < kOutCols && col0 + c0 < P.N; c0 += 64) {
-          const int cols = P.N - col0 - c0;      // columns left, of which this chunk takes 64
-          uint8_t* s0 = slots;
-          if (EPI == kEpiStore) {
-            s0 = slots + (chunk++ & 1) * kDSlotBytes;
-            if (lane == 0) bulk_wait_read<1>();  // the store before last has read its slot
-          } else {
-            if (lane == 0) bulk_wait_read<0>();
-          }
+      for (int cc = first; cc < chunks; cc += kTurns, ++chunk) {
+        const int c0 = cc * kCols;
+        if constexpr (EPI == kEpiStore) {
+          if (lane == 0) bulk_wait_read<1>();    // the store before last has read its slot
           __syncwarp();
+          uint8_t* s0 = slots + (chunk & 1) * kDSlotBytes;
 #pragma unroll
           for (int hf = 0; hf < 2; ++hf) {
             const int c = c0 + hf * 32;
             float v[32];
             tmem_ld16(tb + c, v);
             tmem_ld16(tb + c + 16, v + 16);
-            if constexpr (EPI == kEpiStore) {
-              tmem_ld_wait();
-              if constexpr (LORA) {
-                if (poison && row < P.M) {
+            tmem_ld_wait();
+            if constexpr (LORA) {
+              if (poison && row < P.M) {
 #pragma unroll
-                  for (int j = 0; j < 32; ++j)
-                    if (hf * 32 + j < cols) v[j] += lora_nonfinite_term(g.lora, row, col0 + c + j);
-                }
+                for (int j = 0; j < 32; ++j)
+                  if (col0 + c + j < P.N) v[j] += lora_nonfinite_term(g.lora, row, col0 + c + j);
               }
-              uint32_t w[16];
-#pragma unroll
-              for (int j = 0; j < 16; ++j) w[j] = pack_bf16(v[2 * j], v[2 * j + 1]);
-              stage_half(s0, lane, hf, w);
-            } else if constexpr (EPI == kEpiGated) {
-              float u[32];
-              tmem_ld16(tb + BN / 2 + c, u);
-              tmem_ld16(tb + BN / 2 + c + 16, u + 16);
-              tmem_ld_wait();
-              uint32_t w[16];
-              if (g.keep) {
-#pragma unroll
-                for (int j = 0; j < 16; ++j) w[j] = pack_bf16(v[2 * j], v[2 * j + 1]);
-                stage_half(slots + kDSlotBytes, lane, hf, w);
-#pragma unroll
-                for (int j = 0; j < 16; ++j) w[j] = pack_bf16(u[2 * j], u[2 * j + 1]);
-                stage_half(slots + 2 * kDSlotBytes, lane, hf, w);
-              }
-#pragma unroll
-              for (int j = 0; j < 16; ++j)
-                w[j] = pack_bf16(act_value(v[2 * j], g.act) * u[2 * j], act_value(v[2 * j + 1], g.act) * u[2 * j + 1]);
-              stage_half(s0, lane, hf, w);
-            } else {
-              // g and u of this row: 32 columns are 64 bytes of each (N is a multiple of 128)
-              uint4 gv[4], uv[4];
-              const uint16_t* pg = g.pre + static_cast<size_t>(row) * (2 * static_cast<size_t>(P.N)) + col0 + c;
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                gv[k] = row < P.M ? __ldg(reinterpret_cast<const uint4*>(pg) + k) : make_uint4(0, 0, 0, 0);
-                uv[k] = row < P.M ? __ldg(reinterpret_cast<const uint4*>(pg + P.N) + k) : make_uint4(0, 0, 0, 0);
-              }
-              tmem_ld_wait();
-              const uint32_t* gw = reinterpret_cast<const uint32_t*>(gv);
-              const uint32_t* uw = reinterpret_cast<const uint32_t*>(uv);
-              uint32_t wg[16], wu[16], wh[16];
-#pragma unroll
-              for (int j = 0; j < 16; ++j) {
-                float dg[2], du[2], h[2];
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                  const float z = __uint_as_float(e ? gw[j] & 0xffff0000u : gw[j] << 16);
-                  const float u = __uint_as_float(e ? uw[j] & 0xffff0000u : uw[j] << 16);
-                  act_gradient(z, u, v[2 * j + e], g.act, dg[e], du[e], h[e]);
-                }
-                wg[j] = pack_bf16(dg[0], dg[1]);
-                wu[j] = pack_bf16(du[0], du[1]);
-                wh[j] = pack_bf16(h[0], h[1]);
-              }
-              stage_half(slots, lane, hf, wg);
-              stage_half(slots + kDSlotBytes, lane, hf, wu);
-              if (g.keep) stage_half(slots + 2 * kDSlotBytes, lane, hf, wh);
             }
+            uint32_t w[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) w[j] = pack_bf16(v[2 * j], v[2 * j + 1]);
+            stage_half(s0, lane, hf, w);
           }
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           __syncwarp();
           if (lane == 0) {
             tma_store_2d(&P.c0, s0, col0 + c0, row0);
-            if (EPI == kEpiDgate || (EPI == kEpiGated && g.keep)) tma_store_2d(&P.c1, slots + kDSlotBytes, col0 + c0, row0);
-            if (EPI != kEpiStore && g.keep) tma_store_2d(&P.c2, slots + 2 * kDSlotBytes, col0 + c0, row0);
+            bulk_commit();
+          }
+        } else {
+          uint8_t* set = slots + (EPI == kEpiDgate ? (chunk & 1) * 3 * kDHalfBytes : 0);
+          float v[32];
+          tmem_ld16(tb + c0, v);
+          tmem_ld16(tb + c0 + 16, v + 16);
+          uint32_t w0[16], w1[16], w2[16];
+          if constexpr (EPI == kEpiGated) {
+            float u[32];
+            tmem_ld16(tb + BN / 2 + c0, u);
+            tmem_ld16(tb + BN / 2 + c0 + 16, u + 16);
+            tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              w1[j] = pack_bf16(v[2 * j], v[2 * j + 1]);
+              w2[j] = pack_bf16(u[2 * j], u[2 * j + 1]);
+              w0[j] = pack_bf16(act_value(v[2 * j], g.act) * u[2 * j], act_value(v[2 * j + 1], g.act) * u[2 * j + 1]);
+            }
+            if (lane == 0) bulk_wait_read<0>();  // the last chunk has left its slots
+          } else {
+            ok = mbar_wait(&pbar[chunk & 1], (chunk >> 1) & 1);
+            if (!__all_sync(0xffffffffu, ok)) break;
+            uint4 gv[4], uv[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              gv[k] = *half_piece(set, lane, k);
+              uv[k] = *half_piece(set + kDHalfBytes, lane, k);
+            }
+            tmem_ld_wait();
+            const uint32_t* gw = reinterpret_cast<const uint32_t*>(gv);
+            const uint32_t* uw = reinterpret_cast<const uint32_t*>(uv);
+            if (lane == 0 && cc + kTurns < chunks) {
+              bulk_wait_read<0>();               // the last chunk has left the other set
+              ask(cc + kTurns, chunk + 1);
+            }
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              float dg[2], du[2], h[2];
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const float z = __uint_as_float(e ? gw[j] & 0xffff0000u : gw[j] << 16);
+                const float u = __uint_as_float(e ? uw[j] & 0xffff0000u : uw[j] << 16);
+                act_gradient(z, u, v[2 * j + e], g.act, dg[e], du[e], h[e]);
+              }
+              w0[j] = pack_bf16(dg[0], dg[1]);
+              w1[j] = pack_bf16(du[0], du[1]);
+              w2[j] = pack_bf16(h[0], h[1]);
+            }
+          }
+          __syncwarp();                          // every lane has read its g and u; the slots are free
+          stage_row(set, lane, w0);
+          if (EPI == kEpiDgate || g.keep) stage_row(set + kDHalfBytes, lane, w1);
+          if (g.keep) stage_row(set + 2 * kDHalfBytes, lane, w2);
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+          if (lane == 0) {
+            tma_store_2d(&P.c0, set, col0 + c0, row0);
+            if (EPI == kEpiDgate || g.keep) tma_store_2d(&P.c1, set + kDHalfBytes, col0 + c0, row0);
+            if (g.keep) tma_store_2d(&P.c2, set + 2 * kDHalfBytes, col0 + c0, row0);
             bulk_commit();
           }
         }
       }
+      if (!__all_sync(0xffffffffu, ok)) break;
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
@@ -475,9 +516,20 @@ inline bool dense_operand_map(CUtensorMap* m, const void* base, bool mn, uint64_
                         mn ? 64 : box_rows);
 }
 
-// Store map: dims {cols, rows}, box {64 columns, 32 rows}; clips what lies outside.
+// Store map of kEpiStore: dims {cols, rows}, box {64 columns, 32 rows}; clips what lies outside.
 inline bool dense_store_map(CUtensorMap* m, void* base, uint64_t cols, uint64_t rows, uint64_t pitch_bytes) {
   return make_map_sw128(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, cols, rows, pitch_bytes, 0, 0, 32);
+}
+
+// Map of a half slot: box {32 columns, 32 rows}, 64-byte swizzle.
+inline bool dense_half_map(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows, uint64_t pitch_bytes) {
+  EncodeTiledFn enc = get_encode_fn();
+  if (!enc) return false;
+  const cuuint64_t dims[2] = {cols, rows}, strides[1] = {pitch_bytes};
+  const cuuint32_t box[2] = {32, 32}, es[2] = {1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, es,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 inline void dense_tiles(DenseProblem& P, int M, int N, int K, int out_cols) {
@@ -503,7 +555,7 @@ inline void dense_schedule(DenseArgs& a) {
 
 template <int EPI, int BN, bool LORA>
 cudaError_t launch_dense(DenseArgs& a, cudaStream_t st) {
-  using S = DenseShape<BN, LORA>;
+  using S = DenseShape<EPI, BN, LORA>;
   dense_schedule(a);
   auto kern = dense_kernel<EPI, BN, LORA>;
   cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(S::kSmem));

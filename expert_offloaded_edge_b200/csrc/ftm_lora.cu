@@ -489,7 +489,7 @@ const char* launch_lora(const LoraCall& c, cudaStream_t st, cudaError_t* cerr) {
   g.out = c.y;
   g.ld = c.ldy;
   g.lora = la;
-  if (!proj_maps(g, c.w, false, c.d_out, c.d_in, 2ull * c.d_in, c.x, 2ull * c.ldx)) return "cuTensorMapEncodeTiled failed";
+  if (!proj_maps(g, c.w, false, c.d_out, c.d_in, 2ull * c.d_in, c.x, false, 2ull * c.ldx)) return "cuTensorMapEncodeTiled failed";
   *cerr = launch_proj<kEpiStore, true>(g, st);
   return *cerr == cudaSuccess ? nullptr : "projection launch failed";
 }
