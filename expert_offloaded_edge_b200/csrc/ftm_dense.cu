@@ -139,8 +139,19 @@ const char* launch_gated_ffn_backward(int act, const void* x, int T, int d, int 
       {dy, h, true, true, d, I, T, rd, rI, dw_d},                // dWd = dy^T h
       {dgu, w, false, true, T, d, 2 * I, 2 * rI, rd, dx},        // dx = dgu Wgu
   };
-  const bool split_w = T >= 512 && pair_tiles(2 * I, d, 256) + pair_tiles(d, I, 256) < num_sms() / 4;
-  const bool split[3] = {split_w, split_w, 2 * I >= 512 && few_tiles(T, d, 256)};
+  // A product of few tiles that is deeper than the others keep the pairs busy for
+  // is split along K instead, in a launch of its own (worth it from 32 blocks of
+  // 64: a pair takes 0.42 us for one, a launch 10 us).
+  long tiles[3], work = 0;
+  int depth[3];
+  for (int i = 0; i < 3; ++i) {
+    tiles[i] = all[i].out ? pair_tiles(all[i].rows, all[i].cols, 256) : 0;
+    depth[i] = (all[i].K + kDBK - 1) / kDBK;
+    work += tiles[i] * depth[i];
+  }
+  const int pairs = num_sms() / 2;
+  const bool split_w = tiles[0] + tiles[1] < pairs / 2 && depth[0] - work / pairs >= 32;
+  const bool split[3] = {split_w, split_w, tiles[2] < pairs / 2 && depth[2] - work / pairs >= 32};
   DenseArgs g = {};
   bool launched = false;
   for (int i = 0; i < 3; ++i) {
