@@ -14,28 +14,22 @@
 // operands of the next products; every sum is fp32.
 //
 // Each product runs on one of two engines: tiles of 256 x 256 on CTA pairs
-// (ftm_dense.cuh), bound by the tensor cores, or, where those tiles are too few
-// to occupy the GPU, 128-row tiles split along K over a cluster (ftm_proj.cuh),
-// bound by the bytes.
+// (ftm_dense.cuh), or, for few tokens, 128 rows of weights at a time
+// (ftm_proj.cuh).
 #include "ftm_proj.cuh"
 
 namespace ftm {
 
-// Tiles of an [M][N] product on the pair engine, and whether they are too few to occupy the GPU.
-static long pair_tiles(int M, int N, int cols) {
-  return static_cast<long>((M + kDTileM - 1) / kDTileM) * ((N + cols - 1) / cols);
-}
-static bool few_tiles(int M, int N, int cols) { return pair_tiles(M, N, cols) < num_sms() / 4; }
+static const char* kMapsFailed = "cuTensorMapEncodeTiled failed";
 
 const char* launch_gated_ffn(int act, const void* x, int T, int d, int I, const void* bank, size_t w_d_off, void* pre,
                              void* h, void* y, cudaStream_t st, cudaError_t* cerr) {
-  static const char* maps = "cuTensorMapEncodeTiled failed";
   const uint8_t* w = static_cast<const uint8_t*>(bank);
   uint8_t* pp = static_cast<uint8_t*>(pre);
   const uint64_t rd = 2ull * d, rI = 2ull * I;          // bytes of a row
   *cerr = cudaSuccess;
   prof_mark(FTM_K_GEMM1, st, false);
-  if (few_tiles(T, I, 128)) {
+  if (proj_fits(T, I, 64)) {
     ProjArgs g = {};
     g.T = T;
     g.M = I;
@@ -45,7 +39,7 @@ const char* launch_gated_ffn(int act, const void* x, int T, int d, int I, const 
     g.out = static_cast<uint16_t*>(h);
     g.ld = I;
     g.pre = static_cast<uint16_t*>(pre);
-    if (!proj_maps(g, w, false, 2ull * I, d, rd, x, false, rd)) return maps;
+    if (!proj_maps(g, w, false, 2ull * I, d, rd, x, rd)) return kMapsFailed;
     *cerr = launch_proj<kEpiGated, false>(g, st);
   } else {
     DenseArgs g = {};
@@ -57,21 +51,21 @@ const char* launch_gated_ffn(int act, const void* x, int T, int d, int I, const 
     P.up_row0 = I;
     if (!dense_operand_map(&P.a, x, false, T, d, rd, 128) || !dense_operand_map(&P.b, w, false, 2ull * I, d, rd, 128) ||
         !dense_half_map(&P.c0, h, I, T, rI))
-      return maps;
-    if (pre && (!dense_half_map(&P.c1, pp, I, T, 2 * rI) || !dense_half_map(&P.c2, pp + rI, I, T, 2 * rI))) return maps;
-    *cerr = launch_dense<kEpiGated, 256, false>(g, st);
+      return kMapsFailed;
+    if (pre && (!dense_half_map(&P.c1, pp, I, T, 2 * rI) || !dense_half_map(&P.c2, pp + rI, I, T, 2 * rI))) return kMapsFailed;
+    *cerr = launch_dense<kEpiGated, false>(g, st);
   }
   prof_mark(FTM_K_GEMM1, st, true);
   if (*cerr != cudaSuccess) return "gate/up launch failed";
   prof_mark(FTM_K_GEMM2, st, false);
-  if (few_tiles(T, d, 256)) {
+  if (proj_fits(T, d, 128)) {
     ProjArgs g = {};
     g.T = T;
     g.M = d;
     g.early = 1;
     g.out = static_cast<uint16_t*>(y);
     g.ld = d;
-    if (!proj_maps(g, w + w_d_off, false, d, I, rI, h, false, rI)) return maps;
+    if (!proj_maps(g, w + w_d_off, false, d, I, rI, h, rI)) return kMapsFailed;
     *cerr = launch_proj<kEpiStore, false>(g, st);
   } else {
     DenseArgs g = {};
@@ -80,8 +74,8 @@ const char* launch_gated_ffn(int act, const void* x, int T, int d, int I, const 
     dense_tiles(Q, T, d, I, 256);
     if (!dense_operand_map(&Q.a, h, false, T, I, rI, 128) ||
         !dense_operand_map(&Q.b, w + w_d_off, false, d, I, rI, 128) || !dense_store_map(&Q.c0, y, d, T, rd))
-      return maps;
-    *cerr = launch_dense<kEpiStore, 256, false>(g, st);
+      return kMapsFailed;
+    *cerr = launch_dense<kEpiStore, false>(g, st);
   }
   prof_mark(FTM_K_GEMM2, st, true);
   return *cerr == cudaSuccess ? nullptr : "down launch failed";
@@ -91,12 +85,11 @@ const char* launch_gated_ffn(int act, const void* x, int T, int d, int I, const 
 const char* launch_gated_ffn_backward(int act, const void* x, int T, int d, int I, const void* bank, size_t w_d_off,
                                       const void* pre, const void* dy, void* dx, void* dw_gu, void* dw_d, void* dgu,
                                       void* h, cudaStream_t st, cudaError_t* cerr) {
-  static const char* maps = "cuTensorMapEncodeTiled failed";
   const uint8_t* w = static_cast<const uint8_t*>(bank);
   uint8_t* dg = static_cast<uint8_t*>(dgu);
   const uint64_t rd = 2ull * d, rI = 2ull * I;
   *cerr = cudaSuccess;
-  if (few_tiles(T, I, 256)) {
+  if (proj_fits(T, I, 128)) {
     ProjArgs g = {};
     g.T = T;
     g.M = I;
@@ -106,7 +99,7 @@ const char* launch_gated_ffn_backward(int act, const void* x, int T, int d, int 
     g.ld = 2ll * I;
     g.pre = static_cast<uint16_t*>(const_cast<void*>(pre));
     g.h = static_cast<uint16_t*>(h);
-    if (!proj_maps(g, w + w_d_off, true, I, d, rI, dy, false, rd)) return maps;
+    if (!proj_maps(g, w + w_d_off, true, I, d, rI, dy, rd)) return kMapsFailed;
     *cerr = launch_proj<kEpiDgate, false>(g, st);
   } else {
     DenseArgs g = {};
@@ -121,12 +114,11 @@ const char* launch_gated_ffn_backward(int act, const void* x, int T, int d, int 
         !dense_half_map(&P.c0, dg, I, T, 2 * rI) || !dense_half_map(&P.c1, dg + rI, I, T, 2 * rI) ||
         !dense_half_map(&P.c2, h, I, T, rI) || !dense_half_map(&P.p0, pp, I, T, 2 * rI) ||
         !dense_half_map(&P.p1, pp + rI, I, T, 2 * rI))
-      return maps;
-    *cerr = launch_dense<kEpiDgate, 256, false>(g, st);
+      return kMapsFailed;
+    *cerr = launch_dense<kEpiDgate, false>(g, st);
   }
   if (*cerr != cudaSuccess) return "activation gradient launch failed";
-  // The products.  Each is out[rows][cols] = P Q^T over depth K; those too
-  // small for the pair engine's tiles, but deep, run split along K instead.
+  // The products.  Each is out[rows][cols] = P Q^T over depth K.
   struct Product {
     const void *p, *q;                 // [rows][K] and [cols][K], or stored [K][...] where mn
     bool p_mn, q_mn;
@@ -139,51 +131,56 @@ const char* launch_gated_ffn_backward(int act, const void* x, int T, int d, int 
       {dy, h, true, true, d, I, T, rd, rI, dw_d},                // dWd = dy^T h
       {dgu, w, false, true, T, d, 2 * I, 2 * rI, rd, dx},        // dx = dgu Wgu
   };
-  // A product of few tiles that is deeper than the others keep the pairs busy for
-  // is split along K instead, in a launch of its own (worth it from 32 blocks of
-  // 64: a pair takes 0.42 us for one, a launch 10 us).
-  long tiles[3], work = 0;
-  int depth[3];
-  for (int i = 0; i < 3; ++i) {
-    tiles[i] = all[i].out ? pair_tiles(all[i].rows, all[i].cols, 256) : 0;
-    depth[i] = (all[i].K + kDBK - 1) / kDBK;
-    work += tiles[i] * depth[i];
-  }
-  const int pairs = num_sms() / 2;
-  const bool split_w = tiles[0] + tiles[1] < pairs / 2 && depth[0] - work / pairs >= 32;
-  const bool split[3] = {split_w, split_w, tiles[2] < pairs / 2 && depth[2] - work / pairs >= 32};
-  DenseArgs g = {};
-  bool launched = false;
-  for (int i = 0; i < 3; ++i) {
-    const Product& P = all[i];
-    if (!P.out || split[i]) continue;
-    DenseProblem& Q = g.p[g.n++];
+  // One launch holds all, but for a product of few tiles that is deeper than the
+  // others keep the pairs busy for: in a launch of its own it is split along K
+  // (worth it from 24 blocks of 64: a pair takes 0.42 us for one, a launch 6 us).
+  DenseProblem problems[3];
+  long work = 0;
+  int n = 0;
+  for (const Product& P : all) {
+    if (!P.out) continue;
+    DenseProblem& Q = problems[n++];
+    Q = {};
     dense_tiles(Q, P.rows, P.cols, P.K, 256);
     Q.a_mn = P.p_mn;
     Q.b_mn = P.q_mn;
+    work += static_cast<long>(Q.tiles) * Q.kb;
     if (!dense_operand_map(&Q.a, P.p, P.p_mn, P.rows, P.K, P.p_pitch, 128) ||
-        !dense_operand_map(&Q.b, P.q, P.q_mn, P.cols, P.K, P.q_pitch, 0) ||
+        !dense_operand_map(&Q.b, P.q, P.q_mn, P.cols, P.K, P.q_pitch, 128) ||
         !dense_store_map(&Q.c0, P.out, P.cols, P.rows, 2ull * P.cols))
-      return maps;
+      return kMapsFailed;
+  }
+  const int pairs = num_sms() / 2;
+  DenseArgs g = {};
+  int alone[3], n_alone = 0;
+  for (int i = 0; i < n; ++i) {
+    const DenseProblem& Q = problems[i];
+    if (Q.tiles <= pairs / 2 && Q.kb - work / pairs >= 24) alone[n_alone++] = i;
+    else g.p[g.n++] = Q;
   }
   if (g.n) {
-    *cerr = launch_dense<kEpiStore, 256, false>(g, st);
+    *cerr = launch_dense<kEpiStore, false>(g, st);
     if (*cerr != cudaSuccess) return "gradient products launch failed";
-    launched = true;
   }
-  for (int i = 0; i < 3; ++i) {
-    const Product& P = all[i];
-    if (!P.out || !split[i]) continue;
-    ProjArgs s = {};
-    s.T = P.rows;
-    s.M = P.cols;
-    s.early = launched ? 2 : 0;        // the first waits for dg, du and h, those behind it for nothing but the end
-    s.out = static_cast<uint16_t*>(P.out);
-    s.ld = P.cols;
-    if (!proj_maps(s, P.q, P.q_mn, P.cols, P.K, P.q_pitch, P.p, P.p_mn, P.p_pitch)) return maps;
-    *cerr = launch_proj<kEpiStore, false>(s, st);
+  for (int i = 0; i < n_alone; ++i) {
+    const bool early = g.n || i > 0;   // the first waits for dg, du and h, those behind it for nothing but the end
+    if (dx && alone[i] == n - 1 && proj_fits(T, d, 128)) {
+      ProjArgs s = {};
+      s.T = T;
+      s.M = d;
+      s.early = early ? 2 : 0;
+      s.out = static_cast<uint16_t*>(dx);
+      s.ld = d;
+      if (!proj_maps(s, w, true, d, 2ull * I, rd, dgu, 2 * rI)) return kMapsFailed;
+      *cerr = launch_proj<kEpiStore, false>(s, st);
+    } else {
+      DenseArgs s = {};
+      s.n = 1;
+      s.p[0] = problems[alone[i]];
+      s.early = early;
+      *cerr = launch_dense<kEpiStore, false>(s, st);
+    }
     if (*cerr != cudaSuccess) return "gradient product launch failed";
-    launched = true;
   }
   return nullptr;
 }

@@ -156,6 +156,16 @@ __device__ __forceinline__ void umma2_f16(uint32_t d_tmem, uint64_t a_desc, uint
       : "memory");
 }
 
+// The same for the pair whose even CTA has rank `even` in its cluster.
+__device__ __forceinline__ void umma2_commit_pair(uint64_t* bar, uint32_t even) {
+  const uint16_t mask = static_cast<uint16_t>(0x3u << even);
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+          smem_u32(bar)),
+      "h"(mask)
+      : "memory");
+}
+
 struct TileInfo {
   int g, m, n, rows, row0;
 };

@@ -457,14 +457,12 @@ static cudaError_t launch_shrink_for(const ShrinkArgs& p, cudaStream_t st) {
 const char* launch_lora(const LoraCall& c, cudaStream_t st, cudaError_t* cerr) {
   const int rp = (c.rank + 15) / 16 * 16;
   *cerr = cudaSuccess;
-  const int BNp = 256;     // the pair engine's column tile
-  const long pair_tiles = static_cast<long>((c.T + 255) / 256) * ((c.d_out + BNp - 1) / BNp);
-  const bool pairs = pair_tiles >= num_sms() / 4;
+  const bool pairs = !proj_fits(c.T, c.d_out, 128);
 
   // v first
   const size_t wb = 2ull * c.d_in * c.d_out;
   const ShrinkArgs p = {c.x, c.ldx, c.T, c.d_in, c.a, c.scale, c.ids, c.n, c.rank, rp, c.v,
-                        reinterpret_cast<const uint8_t*>(c.w), !pairs && wb <= kPrefetchBytes ? wb : 0};
+                        reinterpret_cast<const uint8_t*>(c.w), wb <= kPrefetchBytes && c.T <= kShrinkWindow ? wb : 0};
   *cerr = launch_shrink_for(p, st);
   if (*cerr != cudaSuccess) return "adapter shrink launch failed";
 
@@ -473,13 +471,13 @@ const char* launch_lora(const LoraCall& c, cudaStream_t st, cudaError_t* cerr) {
     DenseArgs g = {};
     g.n = 1;
     DenseProblem& P = g.p[0];
-    dense_tiles(P, c.T, c.d_out, c.d_in, BNp);
+    dense_tiles(P, c.T, c.d_out, c.d_in, 256);
     if (!dense_operand_map(&P.a, c.x, false, c.T, c.d_in, 2ull * c.ldx, 128) ||
-        !dense_operand_map(&P.b, c.w, false, c.d_out, c.d_in, 2ull * c.d_in, BNp / 2) ||
+        !dense_operand_map(&P.b, c.w, false, c.d_out, c.d_in, 2ull * c.d_in, 128) ||
         !dense_store_map(&P.c0, c.y, c.d_out, c.T, 2ull * c.ldy))
       return "cuTensorMapEncodeTiled failed";
     g.lora = la;
-    *cerr = launch_dense<kEpiStore, 256, true>(g, st);
+    *cerr = launch_dense<kEpiStore, true>(g, st);
     return *cerr == cudaSuccess ? nullptr : "projection launch failed";
   }
   ProjArgs g = {};
@@ -489,7 +487,7 @@ const char* launch_lora(const LoraCall& c, cudaStream_t st, cudaError_t* cerr) {
   g.out = c.y;
   g.ld = c.ldy;
   g.lora = la;
-  if (!proj_maps(g, c.w, false, c.d_out, c.d_in, 2ull * c.d_in, c.x, false, 2ull * c.ldx)) return "cuTensorMapEncodeTiled failed";
+  if (!proj_maps(g, c.w, false, c.d_out, c.d_in, 2ull * c.d_in, c.x, 2ull * c.ldx)) return "cuTensorMapEncodeTiled failed";
   *cerr = launch_proj<kEpiStore, true>(g, st);
   return *cerr == cudaSuccess ? nullptr : "projection launch failed";
 }

@@ -17,7 +17,6 @@
 // Shared memory stays under half an SM's for BN <= 64, so that the next launch
 // of the chain may move in early and load its weights while this one drains.
 #pragma once
-#include <stdlib.h>
 
 #include "ftm_dense.cuh"
 
@@ -28,11 +27,10 @@ constexpr int kProjThreads = 192;   // warp 0 TMA, warp 1 MMA, warps 2-5 adapter
 struct ProjArgs {
   CUtensorMap a, x;        // weights (boxes of 64 rows x 64 deep, either majorness), tokens {K, T}
   int T, M, kb;            // tokens, outputs, 64-deep blocks
-  int a_mn, x_mn;          // A, X stored rows-innermost (x_mn: tiles of 128 tokens only)
+  int a_mn;                // A stored rows-innermost
   int up_row0;             // gated: first up row of A
   int act, keep;
-  int early;               // the launch before is this library's own, of the same call, and waited for everything
-                           // before it: 1: A may be read before it ends, 2: X too
+  int early;               // the launch before is this call's own, and waited: 1: A may be read before it ends, 2: X too
   uint16_t* out;           // [T][ld]
   int64_t ld;
   uint16_t* pre;           // gated: g, u [T][2M] when kept; dgate: read
@@ -137,21 +135,15 @@ __global__ void __launch_bounds__(kProjThreads, 1) proj_kernel(const __grid_cons
           mbar_arrive_expect_tx(&full_bar[stage], kATileBytes + BN * 128);
           load_a(kb, stage);
         }
-        uint8_t* sx = smem + static_cast<size_t>(stage) * S::kStage + kATileBytes;
-        if (BN == 128 && a.x_mn) {
-          tma_load_2d(sx, &a.x, &full_bar[stage], n0, kb * 64);
-          tma_load_2d(sx + 8192, &a.x, &full_bar[stage], n0 + 64, kb * 64);
-        } else {
-          tma_load_2d(sx, &a.x, &full_bar[stage], kb * 64, n0);
-        }
+        tma_load_2d(smem + static_cast<size_t>(stage) * S::kStage + kATileBytes, &a.x, &full_bar[stage], kb * 64, n0);
         if (++stage == S::kStages) { stage = 0; phase ^= 1u; }
       }
     }
     __syncwarp();
   } else if (warp == 1) {
     if (lane == 0) {
-      const bool amn = a.a_mn, xmn = BN == 128 && a.x_mn;
-      const uint32_t idesc = kIdesc | (amn ? 1u << 15 : 0u) | (xmn ? 1u << 16 : 0u);
+      const bool amn = a.a_mn;
+      const uint32_t idesc = kIdesc | (amn ? 1u << 15 : 0u);
       int stage = 0;
       uint32_t phase = 0;
       bool ok = true;
@@ -162,8 +154,7 @@ __global__ void __launch_bounds__(kProjThreads, 1) proj_kernel(const __grid_cons
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)
           umma_f16(tmem_base, amn ? smem_desc_mn_sw128(sa + kk * 2048) : smem_desc_sw128(sa + kk * 32),
-                   xmn ? smem_desc_mn_sw128(sa + kATileBytes + kk * 2048) : smem_desc_sw128(sa + kATileBytes + kk * 32),
-                   idesc, kb != kb0 || kk != 0 ? 1u : 0u);
+                   smem_desc_sw128(sa + kATileBytes + kk * 32), idesc, kb != kb0 || kk != 0 ? 1u : 0u);
         umma_commit(&empty_bar[stage]);
         if (++stage == S::kStages) { stage = 0; phase ^= 1u; }
       }
@@ -349,7 +340,7 @@ inline int proj_tile(int T) { return T <= 16 ? 16 : T <= 32 ? 32 : T <= 64 ? 64 
 
 template <int EPI, bool LORA>
 cudaError_t launch_proj(const ProjArgs& a, cudaStream_t st) {
-  switch (a.x_mn ? 128 : proj_tile(a.T)) {
+  switch (proj_tile(a.T)) {
     case 16: return launch_proj_bn<EPI, 16, LORA>(a, st);
     case 32: return launch_proj_bn<EPI, 32, LORA>(a, st);
     case 64: return launch_proj_bn<EPI, 64, LORA>(a, st);
@@ -357,14 +348,23 @@ cudaError_t launch_proj(const ProjArgs& a, cudaStream_t st) {
   }
 }
 
-// Maps of the weights [w_rows][K] (a_mn: stored [K][w_rows]) and the tokens [T][K] (x_mn: stored [K][T]).
+// Whether a product of T tokens and M outputs (`rows` of them to a tile) runs
+// here: while its tiles leave room for a split over at least two CTAs each.
+// Beyond, its 128 x 128 tiles are bound by what they read from L2 (6.7 TB/s),
+// twice what the pair engine's read: 512 tokens x 4096 outputs x 4096 take 45 us
+// here, 33 there; 200 x 4096 x 2048 takes 10 here, 12 there.
+inline bool proj_fits(int T, int M, int rows) {
+  const int bn = proj_tile(T);
+  return static_cast<long>((M + rows - 1) / rows) * ((T + bn - 1) / bn) <= num_sms() / 2;
+}
+
+// Maps of the weights [w_rows][K] (a_mn: stored [K][w_rows]) and the tokens [T][K].
 inline bool proj_maps(ProjArgs& a, const void* w, bool a_mn, uint64_t w_rows, uint64_t K, uint64_t w_pitch,
-                      const void* x, bool x_mn, uint64_t x_pitch) {
+                      const void* x, uint64_t x_pitch) {
   a.a_mn = a_mn;
-  a.x_mn = x_mn;
   a.kb = static_cast<int>((K + 63) / 64);
   return dense_operand_map(&a.a, w, a_mn, w_rows, K, w_pitch, 64) &&
-         dense_operand_map(&a.x, x, x_mn, a.T, K, x_pitch, proj_tile(a.T));
+         dense_operand_map(&a.x, x, false, a.T, K, x_pitch, proj_tile(a.T));
 }
 
 }  // namespace ftm
