@@ -53,7 +53,7 @@ const char* launch_gated_ffn(int act, const void* x, int T, int d, int I, const 
         !dense_half_map(&P.c0, h, I, T, rI))
       return kMapsFailed;
     if (pre && (!dense_half_map(&P.c1, pp, I, T, 2 * rI) || !dense_half_map(&P.c2, pp + rI, I, T, 2 * rI))) return kMapsFailed;
-    *cerr = launch_dense<kEpiGated, false>(g, st);
+    *cerr = launch_dense<kEpiGated, false>(g, true, st);
   }
   prof_mark(FTM_K_GEMM1, st, true);
   if (*cerr != cudaSuccess) return "gate/up launch failed";
@@ -75,7 +75,7 @@ const char* launch_gated_ffn(int act, const void* x, int T, int d, int I, const 
     if (!dense_operand_map(&Q.a, h, false, T, I, rI, 128) ||
         !dense_operand_map(&Q.b, w + w_d_off, false, d, I, rI, 128) || !dense_store_map(&Q.c0, y, d, T, rd))
       return kMapsFailed;
-    *cerr = launch_dense<kEpiStore, false>(g, st);
+    *cerr = launch_dense<kEpiStore, false>(g, true, st);
   }
   prof_mark(FTM_K_GEMM2, st, true);
   return *cerr == cudaSuccess ? nullptr : "down launch failed";
@@ -115,7 +115,7 @@ const char* launch_gated_ffn_backward(int act, const void* x, int T, int d, int 
         !dense_half_map(&P.c2, h, I, T, rI) || !dense_half_map(&P.p0, pp, I, T, 2 * rI) ||
         !dense_half_map(&P.p1, pp + rI, I, T, 2 * rI))
       return kMapsFailed;
-    *cerr = launch_dense<kEpiDgate, false>(g, st);
+    *cerr = launch_dense<kEpiDgate, false>(g, true, st);
   }
   if (*cerr != cudaSuccess) return "activation gradient launch failed";
   // The products.  Each is out[rows][cols] = P Q^T over depth K.
@@ -134,41 +134,45 @@ const char* launch_gated_ffn_backward(int act, const void* x, int T, int d, int 
   // One launch holds all, but for a product of few tiles that is deeper than the
   // others keep the pairs busy for: in a launch of its own it is split along K
   // (worth it from 24 blocks of 64: a pair takes 0.42 us for one, a launch 6 us).
+  // The choice looks at all three, so that a gradient has the same bits whichever
+  // others are asked for.
   DenseProblem problems[3];
+  bool alone[3];
   long work = 0;
-  int n = 0;
-  for (const Product& P : all) {
-    if (!P.out) continue;
-    DenseProblem& Q = problems[n++];
+  for (int i = 0; i < 3; ++i) {
+    const Product& P = all[i];
+    DenseProblem& Q = problems[i];
     Q = {};
     dense_tiles(Q, P.rows, P.cols, P.K, 256);
     Q.a_mn = P.p_mn;
     Q.b_mn = P.q_mn;
     work += static_cast<long>(Q.tiles) * Q.kb;
-    if (!dense_operand_map(&Q.a, P.p, P.p_mn, P.rows, P.K, P.p_pitch, 128) ||
-        !dense_operand_map(&Q.b, P.q, P.q_mn, P.cols, P.K, P.q_pitch, 128) ||
-        !dense_store_map(&Q.c0, P.out, P.cols, P.rows, 2ull * P.cols))
+    if (P.out && (!dense_operand_map(&Q.a, P.p, P.p_mn, P.rows, P.K, P.p_pitch, 128) ||
+                  !dense_operand_map(&Q.b, P.q, P.q_mn, P.cols, P.K, P.q_pitch, 128) ||
+                  !dense_store_map(&Q.c0, P.out, P.cols, P.rows, 2ull * P.cols)))
       return kMapsFailed;
   }
   const int pairs = num_sms() / 2;
   DenseArgs g = {};
-  int alone[3], n_alone = 0;
-  for (int i = 0; i < n; ++i) {
+  for (int i = 0; i < 3; ++i) {
     const DenseProblem& Q = problems[i];
-    if (Q.tiles <= pairs / 2 && Q.kb - work / pairs >= 24) alone[n_alone++] = i;
-    else g.p[g.n++] = Q;
+    alone[i] = Q.tiles <= pairs / 2 && Q.kb - work / pairs >= 24;
+    if (all[i].out && !alone[i]) g.p[g.n++] = Q;
   }
+  bool launched = false;
   if (g.n) {
-    *cerr = launch_dense<kEpiStore, false>(g, st);
+    *cerr = launch_dense<kEpiStore, false>(g, false, st);
     if (*cerr != cudaSuccess) return "gradient products launch failed";
+    launched = true;
   }
-  for (int i = 0; i < n_alone; ++i) {
-    const bool early = g.n || i > 0;   // the first waits for dg, du and h, those behind it for nothing but the end
-    if (dx && alone[i] == n - 1 && proj_fits(T, d, 128)) {
+  for (int i = 0; i < 3; ++i) {
+    if (!all[i].out || !alone[i]) continue;
+    // the first waits for dg, du and h, those behind it for nothing but the end
+    if (i == 2 && proj_fits(T, d, 128)) {
       ProjArgs s = {};
       s.T = T;
       s.M = d;
-      s.early = early ? 2 : 0;
+      s.early = launched ? 2 : 0;
       s.out = static_cast<uint16_t*>(dx);
       s.ld = d;
       if (!proj_maps(s, w, true, d, 2ull * I, rd, dgu, 2 * rI)) return kMapsFailed;
@@ -176,11 +180,12 @@ const char* launch_gated_ffn_backward(int act, const void* x, int T, int d, int 
     } else {
       DenseArgs s = {};
       s.n = 1;
-      s.p[0] = problems[alone[i]];
-      s.early = early;
-      *cerr = launch_dense<kEpiStore, false>(s, st);
+      s.p[0] = problems[i];
+      s.early = launched;
+      *cerr = launch_dense<kEpiStore, false>(s, true, st);
     }
     if (*cerr != cudaSuccess) return "gradient product launch failed";
+    launched = true;
   }
   return nullptr;
 }

@@ -710,11 +710,11 @@ cudaError_t launch_dense_split(DenseArgs& a, cudaStream_t st) {
   return count_launch(cudaLaunchKernelEx(&cfg, kern, a));
 }
 
-// One product whose tiles leave half the pairs idle is split along K, from 4
+// One product whose tiles leave half the pairs idle may be split along K, from 4
 // blocks of 64 a pair (an exchange costs as much as 4 blocks).
 template <int EPI, bool LORA>
-cudaError_t launch_dense(DenseArgs& a, cudaStream_t st) {
-  const bool split = a.n == 1 && a.p[0].tiles <= num_sms() / 4 && a.p[0].kb >= 8;
+cudaError_t launch_dense(DenseArgs& a, bool may_split, cudaStream_t st) {
+  const bool split = may_split && a.n == 1 && a.p[0].tiles <= num_sms() / 4 && a.p[0].kb >= 8;
   return split ? launch_dense_split<EPI, LORA, true>(a, st) : launch_dense_split<EPI, LORA, false>(a, st);
 }
 

@@ -477,7 +477,7 @@ const char* launch_lora(const LoraCall& c, cudaStream_t st, cudaError_t* cerr) {
         !dense_store_map(&P.c0, c.y, c.d_out, c.T, 2ull * c.ldy))
       return "cuTensorMapEncodeTiled failed";
     g.lora = la;
-    *cerr = launch_dense<kEpiStore, true>(g, st);
+    *cerr = launch_dense<kEpiStore, true>(g, true, st);
     return *cerr == cudaSuccess ? nullptr : "projection launch failed";
   }
   ProjArgs g = {};

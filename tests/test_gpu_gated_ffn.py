@@ -1,0 +1,305 @@
+"""The dense gated feed-forward block and its backward pass on the GPU, against 64-bit references with bounds
+that follow from the arithmetic (tests/dense_util.py)."""
+import pytest
+import torch
+
+import expert_offloaded_edge_b200 as ftm
+from tests import dense_util as du
+
+pytestmark = pytest.mark.gpu
+
+ACT = {"silu": ftm.FTM_ACT_SILU, "gelu": ftm.FTM_ACT_GELU_TANH}
+CANARY = 7.0
+
+
+def layer(d, I):
+    return ftm.LayerDesc(d, 1, 1, I, 0, 1, ftm.FTM_BF16, 0)
+
+
+def normal(seed, *shape, std=1.0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return (torch.randn(*shape, generator=g, device="cuda") * std).to(torch.bfloat16)
+
+
+def guarded(rows, cols):
+    """A matrix with one more row than the call writes, all set to a value that must survive there."""
+    return torch.full((rows + 1, cols), CANARY, dtype=torch.bfloat16, device="cuda")
+
+
+def workspace(nbytes):
+    return torch.empty(max(nbytes, 256), dtype=torch.uint8, device="cuda")
+
+
+class Block:
+    """Inputs and buffers of one block."""
+
+    def __init__(self, T, d, I, act="silu", seed=0, std=1.0):
+        self.T, self.d, self.I, self.act = T, d, I, act
+        self.L = layer(d, I)
+        self.x, self.bank, self.dy = normal(seed, T, d, std=std), normal(seed + 1, 3 * I * d, std=0.05), normal(seed + 2, T, d)
+        self.y, self.pre, self.dx = guarded(T, d), guarded(T, 2 * I), guarded(T, d)
+        self.dbank = torch.full((3 * I * d + 64,), CANARY, dtype=torch.bfloat16, device="cuda")
+        self.ws = workspace(max(ftm.ftm_gated_ffn_workspace_bytes(self.L, T),
+                                ftm.ftm_gated_ffn_backward_workspace_bytes(self.L, T)))
+
+    def forward(self, pre=True, y=None, stream=None):
+        ftm.ftm_gated_ffn(self.L, ACT[self.act], self.x, self.T, self.bank, self.pre if pre else None,
+                          self.y if y is None else y, self.ws, self.ws.numel(), stream)
+
+    def backward(self, dx=True, dbank=True, stream=None):
+        ftm.ftm_gated_ffn_backward(self.L, ACT[self.act], self.x, self.T, self.bank, self.pre, self.dy,
+                                   self.dx if dx else None, self.dbank if dbank else None, self.ws, self.ws.numel(), stream)
+
+    def done(self):
+        torch.cuda.synchronize()
+        assert ftm.ftm_device_status(True) == 0
+
+    def check_forward(self, pre=True):
+        T, I = self.T, self.I
+        (g, u, y), (eg, eu, ey) = du.block_forward(self.x, self.bank, self.d, I, self.act)
+        du.assert_within(self.y[:T], y, ey, "y")
+        assert bool((self.y[T:] == CANARY).all()) and bool((self.pre[T:] == CANARY).all())
+        if pre:
+            du.assert_within(self.pre[:T, :I], g, eg, "g")
+            du.assert_within(self.pre[:T, I:], u, eu, "u")
+        else:
+            assert bool((self.pre == CANARY).all())
+
+    def check_backward(self, dx=True, dbank=True):
+        T, d, I = self.T, self.d, self.I
+        want, bound = du.block_backward(self.x, self.bank, self.pre[:T], self.dy, d, I, self.act)
+        n = 3 * I * d
+        if dx:
+            du.assert_within(self.dx[:T], want[0], bound[0], "dx")
+            assert bool((self.dx[T:] == CANARY).all())
+        else:
+            assert bool((self.dx == CANARY).all())
+        if dbank:
+            du.assert_within(self.dbank[:2 * I * d].view(2 * I, d), want[1], bound[1], "dw_gu")
+            du.assert_within(self.dbank[2 * I * d:n].view(d, I), want[2], bound[2], "dw_d")
+            assert bool((self.dbank[n:] == CANARY).all())
+        else:
+            assert bool((self.dbank == CANARY).all())
+
+
+# few tokens (16, 32, 64, 128 to a tile, K split), many (CTA pairs, split and not), ragged in both directions
+SHAPES = [(1, 128, 128), (2, 256, 128), (16, 128, 384), (17, 384, 256), (33, 256, 128), (64, 640, 128), (65, 128, 640),
+          (127, 256, 256), (129, 384, 128), (255, 128, 128), (300, 896, 384), (513, 1024, 896), (700, 2048, 256),
+          (1025, 384, 128), (2049, 640, 384)]
+
+
+@pytest.mark.parametrize("T,d,I", SHAPES)
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+def test_block_and_gradients(T, d, I, act):
+    b = Block(T, d, I, act, seed=T + d)
+    b.forward()
+    b.done()
+    b.check_forward()
+    b.backward()
+    b.done()
+    b.check_backward()
+
+
+@pytest.mark.parametrize("T,d,I", [(1, 2048, 768), (8, 2048, 768), (32, 6144, 256), (4100, 256, 1280), (20000, 256, 128),
+                                   (9000, 384, 640)])
+def test_model_widths_and_deep_sums(T, d, I):
+    b = Block(T, d, I, "silu", seed=5)
+    b.forward()
+    b.backward()
+    b.done()
+    b.check_forward()
+    b.check_backward()
+
+
+@pytest.mark.parametrize("T", [5, 200, 1100])
+def test_inference_keeps_nothing_and_answers_the_same(T):
+    b = Block(T, 512, 256)
+    b.forward(pre=False)
+    b.done()
+    b.check_forward(pre=False)
+    first = b.y.clone()
+    b.forward(pre=True)
+    b.done()
+    assert torch.equal(first, b.y)
+
+
+@pytest.mark.parametrize("T", [3, 90, 800])
+@pytest.mark.parametrize("dx,dbank", [(True, False), (False, True)])
+def test_one_of_the_gradients(T, dx, dbank):
+    b = Block(T, 384, 256, "gelu")
+    b.forward()
+    b.backward(dx, dbank)
+    b.done()
+    b.check_backward(dx, dbank)
+
+
+def test_no_tokens():
+    b = Block(1, 256, 128)
+    ftm.ftm_gated_ffn(b.L, 0, None, 0, None, None, None, None, 0)
+    ftm.ftm_gated_ffn_backward(b.L, 0, None, 0, None, None, None, None, b.dbank, None, 0)
+    b.done()
+    assert bool((b.y == CANARY).all())
+    assert bool((b.dbank[:3 * 128 * 256] == 0).all()) and bool((b.dbank[3 * 128 * 256:] == CANARY).all())
+
+
+@pytest.mark.parametrize("T", [4, 130, 700])
+def test_a_broken_row_stays_in_its_row(T):
+    """Infinities and NaN in one token's x reach no other token's y, g, u or dx."""
+    b = Block(T, 384, 256)
+    b.forward()
+    b.backward()
+    b.done()
+    y, pre, dx = b.y.clone(), b.pre.clone(), b.dx.clone()
+    bad = T // 2
+    b.x[bad, 3], b.x[bad, 17] = float("nan"), float("inf")
+    b.dy[bad] = float("nan")
+    b.forward()
+    b.backward(dbank=False)
+    b.done()
+    keep = torch.arange(T + 1, device="cuda") != bad
+    assert torch.equal(b.y[keep], y[keep]) and torch.equal(b.pre[keep], pre[keep]) and torch.equal(b.dx[keep], dx[keep])
+    assert bool(b.y[bad].isnan().all()) and bool(b.dx[bad].isnan().all())
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+def test_far_values_of_the_activation(act):
+    """g and u far outside of the activation's curved part, up to where cubes of them overflow: the kept g and u are
+    planted, so the gradients are those of the formula (0 and 1 slopes), never NaN."""
+    T, d, I = 70, 128, 128
+    for T in (70, 600):
+        b = Block(T, d, I, act)
+        b.forward()
+        far = torch.tensor([-1e38, -3e19, -1e6, -200.0, -90.0, -13.0, 13.0, 90.0, 200.0, 1e6, 3e19, 1e38], device="cuda")
+        b.pre[:T, :I] = far[torch.arange(T * I, device="cuda") % far.numel()].view(T, I).to(torch.bfloat16)
+        b.pre[:T, I:] = 0.5
+        b.dy.mul_(1e-3)
+        b.bank[2 * I * d:].mul_(1e-3)
+        b.backward(dbank=False)
+        b.done()
+        assert bool(torch.isfinite(b.dx).all())
+        # slope 0 on the left, 1 on the right (to fp32), so dg is 0 or dh u
+        g, u, dh = b.pre[:T, :I].double(), 0.5, b.dy.double() @ du.split_bank(b.bank, d, I)[2]
+        dgu = torch.cat([torch.where(g > 0, dh * u, torch.zeros_like(dh)), torch.where(g > 0, dh * g, torch.zeros_like(dh))], 1)
+        w = torch.cat(du.split_bank(b.bank, d, I)[:2])
+        want = dgu @ w
+        # -13 and -90 leave up to 13 sigmoid(-13) = 3e-5 of dh in each term
+        bound = (3 * du.U + du.gamma(2 * I)) * (dgu.abs() @ w.abs()) + 2e-4 * (dh.abs() @ (w[:I].abs() + w[I:].abs()))
+        du.assert_within(b.dx[:T], want, bound + du.U * want.abs(), "dx")
+
+
+@pytest.mark.parametrize("T", [9, 300, 1500])
+def test_the_same_call_gives_the_same_bits(T):
+    b = Block(T, 640, 384)
+    outs = []
+    for _ in range(3):
+        b.ws.fill_(255)                  # stale workspaces are never read (0xffff is a NaN)
+        b.forward()
+        b.backward()
+        b.done()
+        outs.append([t.clone() for t in (b.y, b.pre, b.dx, b.dbank)])
+    for o in outs[1:]:
+        assert all(torch.equal(p, q) for p, q in zip(o, outs[0]))
+
+
+def test_two_streams_at_once():
+    blocks = [Block(T, 512, 384, act, seed=T) for T, act in ((40, "silu"), (900, "gelu"))]
+    for b in blocks:
+        b.forward()
+        b.backward()
+        b.done()
+        b.want = [t.clone() for t in (b.y, b.dx, b.dbank)]
+        b.stream = torch.cuda.Stream()
+        for t in (b.y, b.dx, b.dbank):
+            t.fill_(CANARY)
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for b in blocks:
+            b.forward(stream=b.stream)
+            b.backward(stream=b.stream)
+    torch.cuda.synchronize()
+    for b in blocks:
+        assert all(torch.equal(p, q) for p, q in zip((b.y, b.dx, b.dbank), b.want))
+    assert ftm.ftm_device_status(True) == 0
+
+
+@pytest.mark.parametrize("T", [6, 333])
+def test_captured_and_replayed(T):
+    b = Block(T, 512, 384)
+    b.forward()
+    b.backward()
+    b.done()
+    graph = torch.cuda.CUDAGraph()
+    stream = torch.cuda.Stream()
+    with torch.cuda.stream(stream), torch.cuda.graph(graph, stream=stream):
+        b.forward()
+        b.backward()
+    for seed in (50, 60):
+        b.x.copy_(normal(seed, T, 512))
+        b.dy.copy_(normal(seed + 1, T, 512))
+        graph.replay()
+        b.done()
+        b.check_forward()
+        b.check_backward()
+
+
+def test_agrees_with_the_expert_ffn_of_one_expert():
+    """The same bank as the single expert of a routed layer, every token routed to it."""
+    T, d, I = 48, 512, 256
+    b = Block(T, d, I)
+    b.forward(pre=False)
+    L = ftm.LayerDesc(d, 1, 1, I, 0, 1, ftm.FTM_BF16, 0)
+    offsets = torch.tensor([0, T], dtype=torch.int32, device="cuda")
+    perm = torch.arange(T, dtype=torch.int32, device="cuda")
+    slot = torch.zeros(1, dtype=torch.int32, device="cuda")
+    y = torch.empty(T, d, dtype=torch.bfloat16, device="cuda")
+    ws = workspace(ftm.ftm_ffn_workspace_bytes(L, T))
+    ftm.ftm_expert_ffn(L, b.x, T, offsets, perm, slot, b.bank, None, y, ws, ws.numel())
+    b.done()
+    _, (_, _, ey) = du.block_forward(b.x, b.bank, d, I, "silu")
+    du.assert_within(y, b.y[:T].double(), 2 * ey, "expert FFN")      # each is within its bound of the same value
+
+
+def test_gradients_against_differences():
+    """The kernels' gradients along random directions against central differences of the block in 64 bits."""
+    T, d, I, act = 40, 256, 128, "gelu"
+    b = Block(T, d, I, act, seed=9)
+    b.forward()
+    b.backward()
+    b.done()
+    X, B, DY = b.x.double(), b.bank.double(), b.dy.double()
+
+    def loss(x, bank):
+        n = I * d
+        z = x @ bank[:n].view(I, d).T
+        a, _ = du.activation(z, act)
+        return float(((a * (x @ bank[n:2 * n].view(I, d).T)) @ bank[2 * n:].view(d, I).T * DY).sum())
+
+    (_, bound) = du.block_backward(b.x, b.bank, b.pre[:T], b.dy, d, I, act)
+    # the kept g and u are off by U: their effect on the gradients, at most U (1 + |z| slope') in each factor
+    for seed in range(4):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        vx = torch.randn(T, d, generator=g, device="cuda", dtype=torch.float64)
+        vb = torch.randn(3 * I * d, generator=g, device="cuda", dtype=torch.float64)
+        e = 1e-6
+        for v, got, lim, f in ((vx, b.dx[:T].double(), bound[0], lambda s: loss(X + s * vx, B)),
+                               (vb, b.dbank[:3 * I * d].double(),
+                                torch.cat([bound[1].flatten(), bound[2].flatten()]), lambda s: loss(X, B + s * vb))):
+            num = (f(e) - f(-e)) / (2 * e)
+            ana = float((got * v).sum())
+            # errors of the elements and of the direction are independent: 6 standard deviations of the sum, with
+            # 3 bounds for the gradient's own and the kept values' roundings
+            assert abs(num - ana) <= 6 * 3 * float((lim * v).norm()) + 1e-5 * abs(num)
+
+
+def test_wrong_memory_is_refused():
+    b = Block(8, 256, 128)
+    with pytest.raises(ftm.FtmError) as e:
+        ftm.ftm_gated_ffn(b.L, 0, b.x.cpu(), 8, b.bank, None, b.y, b.ws, b.ws.numel())
+    assert e.value.status == 1 and "x is not memory of the current device" in str(e.value)
+    with pytest.raises(ftm.FtmError):
+        ftm.ftm_gated_ffn_backward(b.L, 0, b.x, 8, b.bank, b.pre, b.dy.cpu(), b.dx, b.dbank, b.ws, b.ws.numel())
+    with pytest.raises(ftm.FtmError):
+        ftm.ftm_gated_ffn(b.L, 0, b.x, 8, b.bank, None, b.x, b.ws, b.ws.numel())
+    b.forward()
+    b.done()
+    b.check_forward()
