@@ -105,14 +105,15 @@ __device__ __forceinline__ bool mbar_try_wait(uint64_t* bar, uint32_t parity) {
 }
 
 // Bounded wait for the phase with the given parity.  Returns false when the
-// wait gave up (time limit, or another role of the grid already failed).
+// wait gave up (time limit, or another wait already did; a reported index is no
+// reason, since whoever met it skipped it and went on).
 __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity) {
   if (mbar_try_wait(bar, parity)) return true;
   const uint64_t t0 = globaltimer();
   for (uint32_t it = 1;; ++it) {
     if (mbar_try_wait(bar, parity)) return true;
     if ((it & 255u) == 0) {
-      if (*reinterpret_cast<volatile int32_t*>(&g_dev_status) != 0) return false;
+      if (*reinterpret_cast<volatile int32_t*>(&g_dev_status) == kDevErrTimeout) return false;
       if (globaltimer() - t0 > kWaitLimitNs) {
         atomicExch(&g_dev_status, kDevErrTimeout);
         return false;

@@ -104,7 +104,7 @@ __device__ __forceinline__ bool mbar_wait_cl(uint64_t* bar, uint32_t parity) {
   for (uint32_t it = 1;; ++it) {
     if (mbar_try_wait_cl(bar, parity)) return true;
     if ((it & 255u) == 0) {
-      if (*reinterpret_cast<volatile int32_t*>(&g_dev_status) != 0) return false;
+      if (*reinterpret_cast<volatile int32_t*>(&g_dev_status) == kDevErrTimeout) return false;
       if (globaltimer() - t0 > kWaitLimitNs) {
         atomicExch(&g_dev_status, kDevErrTimeout);
         return false;

@@ -242,6 +242,25 @@ def test_captured_and_replayed(T):
         b.check_backward()
 
 
+@pytest.mark.parametrize("T", [30, 2500])
+def test_a_reported_id_stops_no_later_call(T):
+    """A routed id out of range, reported and not yet read, does not make the waits of later calls give up."""
+    L = ftm.LayerDesc(256, 4, 1, 128, 0, 4, ftm.FTM_BF16, 0)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    ids = torch.full((8,), 77, **i32)
+    ws = workspace(ftm.ftm_permute_workspace_bytes(L, 8))
+    ftm.ftm_permute(L, ids, 8, torch.zeros(4, **i32), torch.zeros(5, **i32), torch.zeros(8, **i32),
+                    torch.zeros(8, **i32), ws, ws.numel())
+    b = Block(T, 4096, 1024, seed=T)
+    for _ in range(3):
+        b.forward()
+        b.backward()
+    torch.cuda.synchronize()
+    assert ftm.ftm_device_status(True) == 2
+    b.check_forward()
+    b.check_backward()
+
+
 def test_agrees_with_the_expert_ffn_of_one_expert():
     """The same bank as the single expert of a routed layer, every token routed to it."""
     T, d, I = 48, 512, 256

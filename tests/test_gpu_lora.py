@@ -99,6 +99,20 @@ def test_ids_out_of_range_take_no_adapter_and_are_reported(T):
     assert ftm.ftm_device_status(True) == 2
 
 
+@pytest.mark.parametrize("T", [50, 500, 2500])
+def test_a_reported_id_stops_no_later_call(T):
+    """The status word keeps a reported id until it is read; calls in between compute all the same (their waits
+    do not take it for a wait that gave up)."""
+    bad = Linear(4, 256, 128, 2, 16)
+    bad.ids[0] = 9
+    bad.run()
+    m = Linear(T, 4096, 4096, 8, 32, "mixed", seed=T)
+    for _ in range(5):
+        m.run()
+    m.done(status=2)
+    m.check()
+
+
 @pytest.mark.parametrize("T,d_out", [(40, 200), (300, 8200), (2500, 2048)])
 def test_slices_of_one_matrix(T, d_out):
     """x and y are column slices of one matrix; the columns around them and the rows behind stay as they were."""
