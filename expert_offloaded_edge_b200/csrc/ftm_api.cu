@@ -1167,7 +1167,8 @@ ftm_status ftm_lora_linear(const ftm_lora_desc* D, const void* x, int64_t ldx, i
     if (!v.p) continue;
     if (!aligned(v.p, 4)) return fail(FTM_ERR_INVALID_ARG, "%s: %s is not 4-byte aligned", who, v.name);
     const uintptr_t lo = reinterpret_cast<uintptr_t>(v.p) & ~uintptr_t{15};
-    b[m++] = {v.name, reinterpret_cast<const void*>(lo), 1, v.bytes, v.bytes, false};
+    const size_t span = v.bytes + (reinterpret_cast<uintptr_t>(v.p) - lo);
+    b[m++] = {v.name, reinterpret_cast<const void*>(lo), 1, span, span, false};
   }
   if ((s = check_bufs(b, m, who))) return s;
   LoraCall c;

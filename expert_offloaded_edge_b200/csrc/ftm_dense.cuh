@@ -245,8 +245,14 @@ __global__ void __launch_bounds__(DenseShape<EPI, LORA>::kThreads, 1)
   if (warp == 0 && lane == 0) {
     for (int p = 0; p < g.n; ++p) { tma_prefetch_desc(&g.p[p].a); tma_prefetch_desc(&g.p[p].b); }
   }
-  if (!g.early) pdl_wait();
-  pdl_trigger();
+  // LORA: the launch before is always the shrink, which waited for everything
+  // earlier before it let this one start: x and W are final, only v is waited
+  // for, by the warps that feed it.  Pairs on SMs that the shrink leaves idle
+  // (the first pairs, which have the most tiles) start at once.
+  if (!LORA) {
+    if (!g.early) pdl_wait();
+    pdl_trigger();
+  }
   tc_fence_before();
   cluster_sync_all();     // barriers initialised and TMEM allocated in every CTA
   tc_fence_after();
@@ -516,7 +522,11 @@ __global__ void __launch_bounds__(DenseShape<EPI, LORA>::kThreads, 1)
       LoraRing ring;
       const LoraArgs& L = g.lora;
       const int e = threadIdx.x - 192;
-      bool ok = true;
+      bool ok = true, waited = false;
+      auto ready = [&] {
+        if (!waited) { pdl_wait(); pdl_trigger(); }
+        waited = true;
+      };
       for (int i = 0, t; ok && (t = dense_tile_at(g, pair, np, i)) >= 0; ++i) {
         const DenseTile ti = dense_decode(g, t);
         const int m0 = ti.m * kDTileM;
@@ -536,6 +546,7 @@ __global__ void __launch_bounds__(DenseShape<EPI, LORA>::kThreads, 1)
         };
         if (nl * (L.rp >> 4) <= kr) {
           // no slice for this pair: one message without data
+          ready();
           const uint32_t slot = ring.count % kLoraRing;
           ok = mbar_wait_cl(&ls.empty[slot], ((ring.count / kLoraRing) & 1u) ^ 1u);
           ok = feed_all(ok);
@@ -552,7 +563,7 @@ __global__ void __launch_bounds__(DenseShape<EPI, LORA>::kThreads, 1)
         }
         ok = lora_feed<128, BN / 2, S::kGroup>(L, ls, ring, ext, 0, 128 * 32, S::kBuf, e, nl, kr, ks,
                                                m0 + static_cast<int>(rank) * 128 + e, (leader ? i0 : i1) >= 0 ? at : -1,
-                                               ti.n * BN + static_cast<int>(rank) * (BN / 2), [] {}, send);
+                                               ti.n * BN + static_cast<int>(rank) * (BN / 2), ready, send);
       }
     }
   }

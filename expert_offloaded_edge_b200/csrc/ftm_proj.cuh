@@ -209,19 +209,46 @@ __global__ void __launch_bounds__(kProjThreads, 1) proj_kernel(const __grid_cons
       // piece (tokens 4 g .. 4 g + 3, outputs of this row's pair): its owner and its place there
       const uint32_t mine = smem_u32(red) + (kr * kParts + er / kRows) * share * 32 + (er & 1) * 16;
       int local = (er % kRows) / 2, owner = 0;
+      constexpr int kStep = BN < 32 ? BN : 32;
 #pragma unroll 1
-      for (int c0 = 0; c0 < valid; c0 += 16) {
-        float f[16];
-        tmem_ld16(tb + c0, f);
+      for (int c0 = 0; c0 < valid; c0 += kStep) {
+        float f[kStep];
+#pragma unroll
+        for (int j = 0; j < kStep; j += 16) tmem_ld16(tb + c0 + j, f + j);
         tmem_ld_wait();
 #pragma unroll
-        for (int j = 0; j < 16; j += 4) {
+        for (int j = 0; j < kStep; j += 4) {
           if (c0 + j < valid) {
             while (local >= share) { local -= share; ++owner; }
             st_cluster_f32x4(mapa_rank(mine + local * 32, owner), f + j);
             local += kPairs;
           }
         }
+      }
+    }
+  }
+  // This thread's pieces, and for the activation's gradient the g and u of the first two, asked for ahead of
+  // the exchange (their latency was 4 us of a 15 us launch).
+  auto place = [&](int i, int& t0, int& m) {
+    const int piece = kr * share + i;
+    t0 = n0 + piece / kPairs * 4;
+    m = w0 + piece % kPairs * 2;
+    return i < share && piece < pieces && m < a.M;
+  };
+  constexpr int kAhead = EPI == kEpiDgate ? 2 : 1;
+  uint32_t kept[kAhead][4][2];
+  if (EPI == kEpiDgate) {
+    pdl_wait();                         // over since the loads began; every thread that reads `pre` asks for itself
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      int t0, m;
+      const bool in = place(threadIdx.x + k * kProjThreads, t0, m);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint16_t* p = a.pre + static_cast<size_t>(t0 + j) * (2 * static_cast<size_t>(a.M)) + m;
+        const bool on = in && t0 + j < a.T;
+        kept[k][j][0] = on ? __ldg(reinterpret_cast<const uint32_t*>(p)) : 0u;
+        kept[k][j][1] = on ? __ldg(reinterpret_cast<const uint32_t*>(p + a.M)) : 0u;
       }
     }
   }
@@ -232,14 +259,12 @@ __global__ void __launch_bounds__(kProjThreads, 1) proj_kernel(const __grid_cons
   tc_fence_after();
   if (warp == 1) tmem_dealloc(tmem_base, S::kTmemCols);
 
-  if (!LORA) pdl_wait();                // over since the loads began; every thread that reads `pre` asks for itself
+  if (!LORA) pdl_wait();                // this launch's end stands for the end of the one before
   bool poison = false;
   if constexpr (LORA) poison = ls.poison[0] != 0;
-  for (int i = threadIdx.x; i < share; i += kProjThreads) {
-    const int piece = kr * share + i;
-    if (piece >= pieces) break;
-    const int t0 = n0 + piece / kPairs * 4, m = w0 + piece % kPairs * 2;
-    if (m >= a.M) continue;
+  auto finish = [&](int i, const uint32_t (*z)[2]) {
+    int t0, m;
+    if (!place(i, t0, m)) return;
     auto sum = [&](int part, float* f) {       // f[output * 4 + token]
 #pragma unroll
       for (int j = 0; j < 8; ++j) f[j] = 0.f;
@@ -276,7 +301,8 @@ __global__ void __launch_bounds__(kProjThreads, 1) proj_kernel(const __grid_cons
           *reinterpret_cast<uint32_t*>(p + a.M) = pack_bf16(u0, u1);
         }
       } else {
-        const uint32_t gw = __ldg(reinterpret_cast<const uint32_t*>(p)), uw = __ldg(reinterpret_cast<const uint32_t*>(p + a.M));
+        const uint32_t gw = z ? z[j][0] : __ldg(reinterpret_cast<const uint32_t*>(p));
+        const uint32_t uw = z ? z[j][1] : __ldg(reinterpret_cast<const uint32_t*>(p + a.M));
         float dg0, dg1, du0, du1, h0, h1;
         act_gradient(__uint_as_float(gw << 16), __uint_as_float(uw << 16), v0, a.act, dg0, du0, h0);
         act_gradient(__uint_as_float(gw & 0xffff0000u), __uint_as_float(uw & 0xffff0000u), v1, a.act, dg1, du1, h1);
@@ -285,7 +311,13 @@ __global__ void __launch_bounds__(kProjThreads, 1) proj_kernel(const __grid_cons
         if (a.keep) *reinterpret_cast<uint32_t*>(a.h + static_cast<size_t>(t) * a.M + m) = pack_bf16(h0, h1);
       }
     }
+  };
+  int i = threadIdx.x;
+  if constexpr (EPI == kEpiDgate) {
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k, i += kProjThreads) finish(i, kept[k]);
   }
+  for (; i < share; i += kProjThreads) finish(i, nullptr);
 }
 
 // ---- host ------------------------------------------------------------------------

@@ -116,6 +116,7 @@ def test_lora_refusals():
     refused(linear(D, y=A), 1, "y overlaps x")
     refused(linear(D, y=A + STEP + 128), 1, "y overlaps w")
     refused(linear(D, y=A + 4 * STEP), 1, "y overlaps adapter_ids")
+    refused(linear(D, ids=A + 5 * STEP - 4), 1, "y overlaps adapter_ids")       # its last three entries
     # column slices of one matrix: 256 + 128 columns of 384 share no byte, 16 columns earlier they do
     refused(linear(D, ldx=384, ldy=384, y=A + 2 * 240), 1, "y overlaps x")
     assert "overlap" not in (linear(D, ldx=384, ldy=384, y=A + 2 * 256) and ftm.ftm_last_error())
