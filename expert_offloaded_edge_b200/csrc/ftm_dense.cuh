@@ -272,7 +272,7 @@ __global__ void __launch_bounds__(DenseShape<EPI, LORA>::kThreads, 1)
   auto finish = [&](const DenseProblem& P, const DenseTile& ti, const bool& poison, auto wait, auto load,
                     auto mine) -> bool {
     const int row0 = ti.m * kDTileM + static_cast<int>(rank) * 128 + q * 32;   // this warp's 32 rows
-    const int row = row0 + lane;
+    [[maybe_unused]] const int row = row0 + lane;
     const int col0 = ti.n * kOutCols;
     const int chunks = row0 < P.M ? (min(kOutCols, P.N - col0) + kCols - 1) / kCols : 0;
     auto next = [&](int cc) {
@@ -518,7 +518,7 @@ __global__ void __launch_bounds__(DenseShape<EPI, LORA>::kThreads, 1)
   } else {
     if constexpr (LORA) {
       // one row of the tile per thread; both CTAs list the adapters of all 256 rows and feed the same slices,
-      // each its own 128 rows of v and its own half of the output columns (SPLIT: every ks-th slice)
+      // each its own 128 rows of v and its own half of the output columns (SPLIT: every ks-th message)
       LoraRing ring;
       const LoraArgs& L = g.lora;
       const int e = threadIdx.x - 192;
@@ -544,7 +544,7 @@ __global__ void __launch_bounds__(DenseShape<EPI, LORA>::kThreads, 1)
             mbar_arrive_remote(mapa_rank(smem_u32(&ls.full[slot]), even));
           }
         };
-        if (nl * (L.rp >> 4) <= kr) {
+        if (lora_messages(nl, L.rp, S::kGroup, kr, ks) == 0) {
           // no slice for this pair: one message without data
           ready();
           const uint32_t slot = ring.count % kLoraRing;

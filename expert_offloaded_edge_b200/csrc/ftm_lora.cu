@@ -197,7 +197,7 @@ struct ShrinkFew {
 };
 
 template <int NJ>
-__global__ void __launch_bounds__(kShrinkThreads, NJ == 8 ? 1 : 2) lora_shrink_few_kernel(const ShrinkArgs p) {
+__global__ void __launch_bounds__(kShrinkThreads, 2) lora_shrink_few_kernel(const ShrinkArgs p) {
   using S = ShrinkFew<NJ>;
   constexpr int NC = S::NC, kOut = S::kOut;
   extern __shared__ __align__(16) float s_dyn[];
@@ -213,11 +213,14 @@ __global__ void __launch_bounds__(kShrinkThreads, NJ == 8 ? 1 : 2) lora_shrink_f
   const int t0 = s.tok[g], t1 = s.tok[g + 8];
   const uint16_t* x0 = t0 >= 0 ? p.x + t0 * p.ldx : nullptr;
   const uint16_t* x1 = t1 >= 0 ? p.x + t1 * p.ldx : nullptr;
+  // items (adapter of the list, NC rows of it) are shared out over blockIdx.y
+  const int groups = (p.rp + NC - 1) / NC;
   int pass = 0;
-  for (int li = blockIdx.y; li < n_list; li += gridDim.y) {
-    const int id = s.list[li];
-    const uint16_t* A = p.a_pool + static_cast<size_t>(id) * p.rank * p.K;
-    for (int n0 = 0; n0 < p.rp; n0 += NC, ++pass) {
+  for (int item = blockIdx.y; item < n_list * groups; item += gridDim.y, ++pass) {
+    {
+      const int li = item / groups, n0 = (item - li * groups) * NC;
+      const int id = s.list[li];
+      const uint16_t* A = p.a_pool + static_cast<size_t>(id) * p.rank * p.K;
       float acc[NJ][4] = {};
       for (int c2 = c_lo + 2 * warp; c2 < c_hi; c2 += 16) {
         uint4 xv[2][2], av[2][NJ];
@@ -442,9 +445,8 @@ static cudaError_t launch_shrink(void (*kern)(ShrinkArgs), const ShrinkArgs& p, 
 static cudaError_t launch_shrink_for(const ShrinkArgs& p, cudaStream_t st) {
   if (p.T <= kShrinkWindow) {
     const int ks = p.T <= 64 ? 8 : 4, clusters = p.T <= 64 ? 28 : 64;
-    return p.rp <= 16   ? launch_shrink<ShrinkFew<2>>(lora_shrink_few_kernel<2>, p, ks, clusters, st)
-           : p.rp <= 32 ? launch_shrink<ShrinkFew<4>>(lora_shrink_few_kernel<4>, p, ks, clusters, st)
-                        : launch_shrink<ShrinkFew<8>>(lora_shrink_few_kernel<8>, p, ks, clusters / 2, st);
+    return p.rp <= 16 ? launch_shrink<ShrinkFew<2>>(lora_shrink_few_kernel<2>, p, ks, clusters, st)
+                      : launch_shrink<ShrinkFew<4>>(lora_shrink_few_kernel<4>, p, ks, clusters, st);
   }
   const int tiles = (p.T + 63) / 64;
   const int ks = tiles <= 15 ? 8 : tiles <= 33 ? 4 : tiles <= 74 ? 2 : 1;

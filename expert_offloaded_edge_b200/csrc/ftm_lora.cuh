@@ -68,8 +68,12 @@ __device__ __forceinline__ int lora_id(const int32_t* ids, int T, int n, int t) 
   return -1;
 }
 
-__device__ __forceinline__ bool bf16_pair_nonfinite(uint32_t w) {
-  return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
+// Nonzero where a bf16 of the pair is an infinity or NaN: an exponent of all ones carries into the sign's place.
+__device__ __forceinline__ uint32_t bf16_pair_nonfinite(uint32_t w) {
+  return ((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
+}
+__device__ __forceinline__ uint32_t bf16x8_nonfinite(uint4 w) {
+  return bf16_pair_nonfinite(w.x) | bf16_pair_nonfinite(w.y) | bf16_pair_nonfinite(w.z) | bf16_pair_nonfinite(w.w);
 }
 __device__ __forceinline__ uint32_t bf16_pair_finite(uint32_t w) {
   if ((w & 0x7f80u) == 0x7f80u) w &= 0xffff0000u;
@@ -166,98 +170,118 @@ __device__ __forceinline__ int lora_list(LoraShared<true>& ls, int e, int i0, in
 // Position in the ring of message buffers.
 struct LoraRing {
   uint32_t count = 0;             // messages passed so far
+  uint32_t dirty = ~0u;           // slots that may hold something else than zeros in this thread's row of v
 };
 
-// Feeds one tile's slices: those with index first, first + stride, ... of the
-// list's adapters x rank / 16, G to a message, so that one round of barriers
-// serves G MMAs.  Row `e` of a v slice is token `tok` when e < NV (`mine`: its
-// adapter's list position, -1 for none); row e of a slice of B is output
-// n0 + e when e < NB.  A slice takes buf_bytes of the message's buffer, the
-// operands at v_at and b_at.  `ready()` is called before v is first read,
-// `send(slot, slices, last, poison)` by thread 0 for a finished message.  Each
-// thread moves its rows of both operands through registers, loaded one message
-// ahead: TMA boxes of 32-byte rows took 2 us a message, this takes 0.6.
+// Feeds one tile's slices, the list's adapters x rank / 16, G neighbouring ones to
+// a message, so that one round of barriers serves G MMAs and a row's 128 bytes
+// are read together; this feed takes messages first, first + stride, ...  Row
+// `e` of a v slice is token `tok` when e < NV (`mine`: its adapter's list
+// position, -1 for none); row e of a slice of B is output n0 + e when e < NB.  A
+// slice takes buf_bytes of the message's buffer, the operands at v_at and b_at.
+// `ready()` is called before v is first read, `send(slot, slices, last, poison)`
+// by thread 0 for a finished message.
+//
+// Each thread moves its rows of both operands through registers, loaded two
+// messages ahead, and asks all its rows of B into L2 while it waits for v: what
+// a mixed batch reads here comes from DRAM, and is all that is left to do by
+// then.  (TMA boxes of 32-byte rows took 2 us a message.)
+__device__ __forceinline__ int lora_messages(int n_list, int rp, int G, int first, int stride) {
+  const int total = (n_list * (rp >> 4) + G - 1) / G;
+  return total > first ? (total - first - 1) / stride + 1 : 0;
+}
+
 template <int NV, int NB, int G, typename Ready, typename Send>
 __device__ __forceinline__ bool lora_feed(const LoraArgs& a, LoraShared<true>& ls, LoraRing& ring, uint8_t* ext,
                                           uint32_t v_at, uint32_t b_at, uint32_t buf_bytes, int e, int n_list,
                                           int first, int stride, int tok, int mine, int n0, Ready ready, Send send) {
   const int per = a.rp >> 4;
   const int total = n_list * per;
-  const int cnt = total > first ? (total - first - 1) / stride + 1 : 0;
-  const int msgs = (cnt + G - 1) / G;
+  const int msgs = lora_messages(n_list, a.rp, G, first, stride);
   const uint4 zero = make_uint4(0, 0, 0, 0);
   const uint4* vrow = reinterpret_cast<const uint4*>(a.v + static_cast<size_t>(tok) * a.rp);
   const bool has_b = e < NB && n0 + e < a.d_out;
   const uint16_t* brow = a.b_pool + (static_cast<size_t>(n0) + e) * a.rank;
   const size_t b_pitch = static_cast<size_t>(a.d_out) * a.rank;      // between adapters
-  uint4 v[G][2], b[G][2];
-  int left = cnt, li = first / per, k = first - li * per;           // the next slice to load
-  auto load_b = [&](int s, int l, int kk) {
-    b[s][0] = b[s][1] = zero;
-    if (has_b) {
-      const uint4* p = reinterpret_cast<const uint4*>(brow + ls.id[ls.list[l]] * b_pitch + kk * 16);
-      b[s][0] = __ldg(p);
-      if (kk * 16 + 8 < a.rank) b[s][1] = __ldg(p + 1);
-    }
-  };
-  auto load_v = [&](int s, int l, int kk) {
-    const bool use = e < NV && mine == l;
-    v[s][0] = use ? vrow[2 * kk] : zero;
-    v[s][1] = use ? vrow[2 * kk + 1] : zero;
-  };
-  // the next message's slices into registers; mask: 1 the rows of B, 2 those of v
-  auto load = [&](int mask, bool advance) {
-    int l = li, kk = k, n = left;
+  auto slices = [&](int m) { return min(G, total - (first + m * stride) * G); };
+  if (has_b)
+    for (int m = 0; m < msgs; ++m)
+      for (int s = 0, sl = (first + m * stride) * G, n = slices(m); s < n; s += 4) {
+        const int l = (sl + s) / per;
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(brow + ls.id[ls.list[l]] * b_pitch + (sl + s - l * per) * 16));
+      }
+  ready();
+  struct Set { uint4 v[G][2], b[G][2]; };
+  Set set[2];
+  auto load = [&](Set& r, int m) {
+    if (m >= msgs) return;
+    const int sl0 = (first + m * stride) * G;
+    int l = sl0 / per, k = sl0 - l * per;
+    const int n = slices(m);
 #pragma unroll
     for (int s = 0; s < G; ++s) {
-      if (n > 0) {
-        if (mask & 1) load_b(s, l, kk);
-        if (mask & 2) load_v(s, l, kk);
-        for (kk += stride; kk >= per; kk -= per) ++l;
-        --n;
+      r.b[s][0] = r.b[s][1] = r.v[s][0] = r.v[s][1] = zero;
+      if (s < n) {
+        if (has_b) {
+          const uint4* p = reinterpret_cast<const uint4*>(brow + ls.id[ls.list[l]] * b_pitch + k * 16);
+          r.b[s][0] = __ldg(p);
+          if (k * 16 + 8 < a.rank) r.b[s][1] = __ldg(p + 1);
+        }
+        if (e < NV && mine == l) {
+          r.v[s][0] = vrow[2 * k];
+          r.v[s][1] = vrow[2 * k + 1];
+        }
+        if (++k == per) { k = 0; ++l; }
       }
     }
-    if (advance) { li = l; k = kk; left = n; }
   };
-  load(1, false);          // B does not depend on the shrink
-  ready();
-  load(2, true);
+  load(set[0], 0);
+  load(set[1], 1);
   bool ok = true;
-  for (int m = 0; m < msgs; ++m) {
+  uint32_t dirty = ring.dirty;               // slots in which this row of v is not all zero
+  auto pass = [&](Set& r, int m) -> bool {
     const uint32_t slot = ring.count % kLoraRing, phase = (ring.count / kLoraRing) & 1u;
     ring.count += 1;
-    const int n = min(G, cnt - m * G);
+    const int n = slices(m);
     ok = ok && mbar_wait_cl(&ls.empty[slot], phase ^ 1u);
     uint8_t* buf = ext + slot * G * buf_bytes;
-    bool bad = false;
     if (ok) {
       const int sw = (e >> 2) & 1;
+      // v: where the token has no slice here and the row is still zero from before, nothing is written
+      const int sl0 = (first + m * stride) * G;
+      const bool any_v = e < NV && mine >= 0 && mine * per < sl0 + n && (mine + 1) * per > sl0;
+      if (e < NV && (any_v || (dirty >> slot & 1u))) {
 #pragma unroll
-      for (int s = 0; s < G; ++s) {
-        if (s < n) {
-          if (e < NV) {
-            uint8_t* row = buf + s * buf_bytes + v_at + e * 32;
-            *reinterpret_cast<uint4*>(row + sw * 16) = v[s][0];
-            *reinterpret_cast<uint4*>(row + (sw ^ 1) * 16) = v[s][1];
-          }
-          if (e < NB) {
-            uint8_t* row = buf + s * buf_bytes + b_at + e * 32;
+        for (int s = 0; s < G; ++s) {
+          uint8_t* row = buf + s * buf_bytes + v_at + e * 32;
+          *reinterpret_cast<uint4*>(row + sw * 16) = r.v[s][0];
+          *reinterpret_cast<uint4*>(row + (sw ^ 1) * 16) = r.v[s][1];
+        }
+        dirty = (dirty & ~(1u << slot)) | (any_v ? 1u << slot : 0u);
+      }
+      if (e < NB) {
+        uint32_t bad = 0;
+#pragma unroll
+        for (int s = 0; s < G; ++s) bad |= bf16x8_nonfinite(r.b[s][0]) | bf16x8_nonfinite(r.b[s][1]);
+        if (bad) {
+          ls.bad[slot] = 1;
+#pragma unroll
+          for (int s = 0; s < G; ++s)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              uint4 w = b[s][h];
-              if (bf16_pair_nonfinite(w.x) || bf16_pair_nonfinite(w.y) || bf16_pair_nonfinite(w.z) ||
-                  bf16_pair_nonfinite(w.w)) {
-                w = make_uint4(bf16_pair_finite(w.x), bf16_pair_finite(w.y), bf16_pair_finite(w.z), bf16_pair_finite(w.w));
-                bad = true;
-              }
-              *reinterpret_cast<uint4*>(row + (sw ^ h) * 16) = w;
+              const uint4 w = r.b[s][h];
+              r.b[s][h] = make_uint4(bf16_pair_finite(w.x), bf16_pair_finite(w.y), bf16_pair_finite(w.z), bf16_pair_finite(w.w));
             }
-          }
+        }
+#pragma unroll
+        for (int s = 0; s < G; ++s) {
+          uint8_t* row = buf + s * buf_bytes + b_at + e * 32;
+          *reinterpret_cast<uint4*>(row + sw * 16) = r.b[s][0];
+          *reinterpret_cast<uint4*>(row + (sw ^ 1) * 16) = r.b[s][1];
         }
       }
     }
-    if (bad) ls.bad[slot] = 1;
-    load(3, true);
+    load(r, m + 2);
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     if (!feed_all(ok)) return false;
     if (e == 0) {
@@ -265,7 +289,13 @@ __device__ __forceinline__ bool lora_feed(const LoraArgs& a, LoraShared<true>& l
       ls.bad[slot] = 0;
       send(slot, static_cast<uint32_t>(n), m + 1 == msgs, any);
     }
+    return true;
+  };
+  for (int m = 0; m < msgs; m += 2) {
+    if (!pass(set[0], m)) return false;
+    if (m + 1 < msgs && !pass(set[1], m + 1)) return false;
   }
+  ring.dirty = dirty;
   return true;
 }
 

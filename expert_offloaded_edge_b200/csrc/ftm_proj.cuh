@@ -68,7 +68,7 @@ __global__ void __launch_bounds__(kProjThreads, 1) proj_kernel(const __grid_cons
 
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t full_bar[S::kStages], empty_bar[S::kStages], tfull_bar, count_bar;
-  __shared__ uint32_t tmem_holder, slices;
+  __shared__ uint32_t tmem_holder, messages;
   __shared__ LoraShared<LORA> ls;
 
   const uint32_t smem_base = (smem_u32(smem_raw) + 1023u) & ~1023u;
@@ -160,12 +160,12 @@ __global__ void __launch_bounds__(kProjThreads, 1) proj_kernel(const __grid_cons
       }
       if constexpr (LORA) {
         ok = ok && mbar_wait(&count_bar, 0);
-        const uint32_t cnt = ok ? slices : 0;
-        for (uint32_t c = 0; c * S::kGroup < cnt; ++c) {
+        const uint32_t cnt = ok ? messages : 0;
+        for (uint32_t c = 0; c < cnt; ++c) {
           const uint32_t slot = c % kLoraRing;
           if (!mbar_wait_cl(&ls.full[slot], (c / kLoraRing) & 1u)) { ok = false; break; }
           tc_fence_after();
-          const uint32_t n = min(static_cast<uint32_t>(S::kGroup), cnt - c * S::kGroup);
+          const uint32_t n = ls.msg[slot];
           for (uint32_t s = 0; s < n; ++s) {
             const uint32_t sb = smem_u32(ext + (slot * S::kGroup + s) * S::kBuf);
             umma_f16(tmem_base, smem_desc_k32(sb), smem_desc_k32(sb + 128 * 32), kIdesc, 1u);
@@ -183,14 +183,14 @@ __global__ void __launch_bounds__(kProjThreads, 1) proj_kernel(const __grid_cons
       const int i0 = e < BN ? lora_id(a.lora.ids, a.T, a.lora.n, n0 + e) : -1;
       int at;
       const int nl = lora_list<128>(ls, e, i0, -1, 0, at);
-      const int total = nl * (a.lora.rp >> 4);
       if (e == 0) {
-        slices = total > kr ? (total - kr - 1) / ks + 1 : 0;
+        messages = lora_messages(nl, a.lora.rp, S::kGroup, kr, ks);
         mbar_arrive(&count_bar);
       }
       LoraRing ring;
-      auto ready = [] { pdl_wait(); pdl_trigger(); };      // the shrink's v
-      auto send = [&](uint32_t slot, uint32_t, bool, bool bad) {
+      auto ready = [] { pdl_wait(); pdl_trigger(); };
+      auto send = [&](uint32_t slot, uint32_t n, bool, bool bad) {
+        ls.msg[slot] = n;
         if (bad)      // every rank's epilogue looks at its own flag
           for (int r = 0; r < ks; ++r)
             asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(mapa_rank(smem_u32(&ls.poison[0]), r)), "r"(kLoraPoison)
