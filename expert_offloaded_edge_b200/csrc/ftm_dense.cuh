@@ -171,10 +171,10 @@ struct DenseShape {
   static constexpr int kEpiWarps = EPI == kEpiStore ? 4 : 8;
   static constexpr uint32_t kWarpStaging = EPI == kEpiStore ? 2 * kDSlotBytes : (EPI == kEpiGated ? 3 : 6) * kDHalfBytes;
   static constexpr uint32_t kStaging = kEpiWarps * kWarpStaging;
-  static constexpr int kGroup = 2;                                 // adapter slices per message
+  static constexpr int kGroup = 4;                                 // adapter slices per message
   static constexpr uint32_t kBuf = 2 * 128 * 32;                   // a slice of v and one of B[a]
   static constexpr uint32_t kExt = LORA ? kLoraRing * kGroup * kBuf : 0;
-  static constexpr int kStages = EPI == kEpiDgate ? 4 : 5;
+  static constexpr int kStages = EPI == kEpiDgate || LORA ? 4 : 5;
   static constexpr size_t kSmem = 1024 + static_cast<size_t>(kStages) * kStage + kStaging + kExt;
   static constexpr int kThreads = 64 + 32 * kEpiWarps + (LORA ? 128 : 0);
 };
