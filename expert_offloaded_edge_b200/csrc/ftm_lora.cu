@@ -280,10 +280,9 @@ template <int NJ>
 struct ShrinkMany {
   static constexpr int MT = 64, NC = 8 * NJ, kOut = MT * NC, kPart = kOut + 64;
   static constexpr int kHalf = (MT + NC) * 128;                      // 64 deep of a stage
-  static constexpr int kStages = NJ == 16 ? 3 : 5;
-  static constexpr size_t kRing = static_cast<size_t>(kStages) * 2 * kHalf;
-  static constexpr size_t kSmem = kRing + static_cast<size_t>(2 * kPart) * 4;
-  static_assert(2 * kOut * 4 <= kRing, "the depth halves' sums take the ring's place");
+  static constexpr int kStages = NJ == 16 ? 4 : 6;
+  static constexpr size_t kSmem = static_cast<size_t>(kStages) * 2 * kHalf;
+  static_assert((2 * kOut + kPart) * 4 <= kSmem, "the sums take the ring's place");
 };
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool in) {
@@ -302,7 +301,7 @@ __global__ void __launch_bounds__(kShrinkThreads, 1) lora_shrink_many_kernel(con
   constexpr int MT = S::MT, NC = S::NC, kOut = S::kOut, kStages = S::kStages;
   extern __shared__ __align__(128) uint8_t s_ring[];
   float* red = reinterpret_cast<float*>(s_ring);                     // [depth half][place][column], when the ring is done
-  float* part = reinterpret_cast<float*>(s_ring + S::kRing);
+  float* part = red + 2 * kOut;                                      // [rank][its share of the outputs]
   __shared__ ShrinkTile<MT> s;
   __shared__ int32_t s_col[NJ], s_r[NJ];                             // 8 columns' adapter (-1: none) and place in v
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -320,8 +319,7 @@ __global__ void __launch_bounds__(kShrinkThreads, 1) lora_shrink_many_kernel(con
 #pragma unroll
   for (int i = 0; i < 2; ++i) xr[i] = s.tok[lr + i * 32] >= 0 ? p.x + s.tok[lr + i * 32] * p.ldx : nullptr;
   const int fit = NC / p.rp;             // adapters of a pass
-  int pass = 0;
-  for (int l0 = blockIdx.y * fit; l0 < n_ad; l0 += fit * gridDim.y, ++pass) {
+  for (int l0 = blockIdx.y * fit; l0 < n_ad; l0 += fit * gridDim.y) {
     if (threadIdx.x < NJ) {
       const int a = 8 * threadIdx.x / p.rp, l = l0 + a;
       s_col[threadIdx.x] = a < fit && l < n_ad ? s.list[l] : -1;
@@ -395,7 +393,8 @@ __global__ void __launch_bounds__(kShrinkThreads, 1) lora_shrink_many_kernel(con
       for (int h = 0; h < 2; ++h)
         *reinterpret_cast<float2*>(&red[wk * kOut + (wm * 16 + h * 8 + g) * NC + j * 8 + 2 * tq]) =
             make_float2(acc[j][2 * h], acc[j][2 * h + 1]);
-    __syncthreads();
+    if (ks > 1) cluster_sync_all();      // every rank's ring is idle: sums may cross
+    else __syncthreads();
     auto halves = [&](int at, float* f) {
       const float4* u = reinterpret_cast<const float4*>(red + at);
       const float4* v = reinterpret_cast<const float4*>(red + kOut + at);
@@ -403,25 +402,27 @@ __global__ void __launch_bounds__(kShrinkThreads, 1) lora_shrink_many_kernel(con
       f[0] = a.x + c.x; f[1] = a.y + c.y; f[2] = a.z + c.z; f[3] = a.w + c.w;
       f[4] = b.x + d.x; f[5] = b.y + d.y; f[6] = b.z + d.z; f[7] = b.w + d.w;
     };
-    shrink_store<MT, NC>(p, s, part + (pass & 1) * S::kPart, ks, kr, halves, [&](int c, int& r) {
+    shrink_store<MT, NC>(p, s, part, ks, kr, halves, [&](int c, int& r) {
       r = s_r[c >> 3];
       return s_col[c >> 3];
     });
-    if (ks > 1) __syncthreads();         // the list of columns is free again
+    if (ks > 1) __syncthreads();         // the ring and the list of columns are free again
   }
 }
 
 // ---------------------------------------------------------------------------
 // Host side
 // ---------------------------------------------------------------------------
-// clusters: of ks blocks, that run at once; what the tiles leave of them shares out a tile's adapters.
+// clusters: of ks blocks, that run at once; what the tiles leave of them, at
+// least `least` blocks a tile, shares out a tile's adapters.
 template <typename S>
-static cudaError_t launch_shrink(void (*kern)(ShrinkArgs), const ShrinkArgs& p, int ks, int clusters, cudaStream_t st) {
+static cudaError_t launch_shrink(void (*kern)(ShrinkArgs), const ShrinkArgs& p, int ks, int clusters, int least,
+                                 cudaStream_t st) {
   cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(S::kSmem));
   if (err != cudaSuccess) return err;
   const int tiles = (p.T + S::MT - 1) / S::MT;
   int split = clusters / tiles;
-  split = split < 1 ? 1 : split > 16 ? 16 : split;
+  split = split < least ? least : split > 16 ? 16 : split;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(ks * tiles, split);
   cfg.blockDim = dim3(kShrinkThreads);
@@ -445,14 +446,17 @@ static cudaError_t launch_shrink(void (*kern)(ShrinkArgs), const ShrinkArgs& p, 
 static cudaError_t launch_shrink_for(const ShrinkArgs& p, cudaStream_t st) {
   if (p.T <= kShrinkWindow) {
     const int ks = p.T <= 64 ? 8 : 4, clusters = p.T <= 64 ? 28 : 64;
-    return p.rp <= 16 ? launch_shrink<ShrinkFew<2>>(lora_shrink_few_kernel<2>, p, ks, clusters, st)
-                      : launch_shrink<ShrinkFew<4>>(lora_shrink_few_kernel<4>, p, ks, clusters, st);
+    return p.rp <= 16 ? launch_shrink<ShrinkFew<2>>(lora_shrink_few_kernel<2>, p, ks, clusters, 1, st)
+                      : launch_shrink<ShrinkFew<4>>(lora_shrink_few_kernel<4>, p, ks, clusters, 1, st);
   }
   const int tiles = (p.T + 63) / 64;
   const int ks = tiles <= 15 ? 8 : tiles <= 33 ? 4 : tiles <= 74 ? 2 : 1;
   const int clusters = ks == 8 ? 15 : ks == 4 ? 33 : ks == 2 ? 74 : 148;
-  return p.rp <= 32 ? launch_shrink<ShrinkMany<8>>(lora_shrink_many_kernel<8>, p, ks, clusters, st)
-                    : launch_shrink<ShrinkMany<16>>(lora_shrink_many_kernel<16>, p, ks, clusters, st);
+  // above 64 columns a pass holds one adapter: a tile over the border of two requests gives the second to a block
+  // of its own (most find none: 2 us, against 57 us of one 128-column pass over 4096)
+  return p.rp <= 32   ? launch_shrink<ShrinkMany<8>>(lora_shrink_many_kernel<8>, p, ks, clusters, 1, st)
+         : p.rp <= 64 ? launch_shrink<ShrinkMany<16>>(lora_shrink_many_kernel<16>, p, ks, clusters, 1, st)
+                      : launch_shrink<ShrinkMany<16>>(lora_shrink_many_kernel<16>, p, ks, clusters, 2, st);
 }
 
 // Returns a message on failure, nullptr on success.
