@@ -1,9 +1,7 @@
 // The dense (ungrouped) bf16 GEMM engine on CTA pairs: D = A B^T over tiles of
 // 256 rows x 256 columns, one tile per pair of CTAs (tcgen05 cta_group::2).
-// Narrower tiles do not pay: at 256 x 128 a pair reads 24 KB per CTA and 64 deep
-// instead of 32 for half the products, and L2 already gives 87 GB/s to every SM
-// (a 4096 x 4096 x 2048 product took 1.9x as long).
-//
+// Narrower tiles do not pay: an MMA of 128 accumulator columns takes as long as
+// one of 256 (a 4096 x 4096 x 2048 product took 1.9x as long in 256 x 128 tiles).
 // Rows (tokens, or the rows of a weight gradient) are on the MMA's M side, so
 // that a thread of the epilogue owns one row and consecutive columns: the
 // gate/up pairing, the activation's gradient and the stores need no exchange

@@ -382,9 +382,9 @@ cudaError_t launch_proj(const ProjArgs& a, cudaStream_t st) {
 
 // Whether a product of T tokens and M outputs (`rows` of them to a tile) runs
 // here: while its tiles leave room for a split over at least two CTAs each.
-// Beyond, its 128 x 128 tiles are bound by what they read from L2 (6.7 TB/s),
-// twice what the pair engine's read: 512 tokens x 4096 outputs x 4096 take 45 us
-// here, 33 there; 200 x 4096 x 2048 takes 10 here, 12 there.
+// Beyond, the pair engine does four times the products in an MMA of the same
+// time and reads half as much from L2 for each: 512 tokens x 4096 outputs x 4096
+// take 45 us here, 33 there; 200 x 4096 x 2048 takes 10 here, 12 there.
 inline bool proj_fits(int T, int M, int rows) {
   const int bn = proj_tile(T);
   return static_cast<long>((M + rows - 1) / rows) * ((T + bn - 1) / bn) <= num_sms() / 2;
