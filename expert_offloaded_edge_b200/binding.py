@@ -137,13 +137,12 @@ def desc_for(cfg) -> LayerDesc:
 
 
 def _ptr(t) -> Optional[int]:
-    if t is None:
-        return None
-    if isinstance(t, int):
+    if t is None or isinstance(t, int):
         return t
-    if hasattr(t, "data_ptr"):
+    try:
         return t.data_ptr()
-    return t.ctypes.data   # numpy array (host)
+    except AttributeError:
+        return t.ctypes.data   # numpy array (host)
 
 
 def _stream(stream) -> Optional[int]:

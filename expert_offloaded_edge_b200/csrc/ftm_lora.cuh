@@ -205,11 +205,15 @@ __device__ __forceinline__ bool lora_feed(const LoraArgs& a, LoraShared<true>& l
   const size_t b_pitch = static_cast<size_t>(a.d_out) * a.rank;      // between adapters
   auto slices = [&](int m) { return min(G, total - (first + m * stride) * G); };
   if (has_b)
-    for (int m = 0; m < msgs; ++m)
-      for (int s = 0, sl = (first + m * stride) * G, n = slices(m); s < n; s += 4) {
-        const int l = (sl + s) / per;
-        asm volatile("prefetch.global.L2 [%0];" ::"l"(brow + ls.id[ls.list[l]] * b_pitch + (sl + s - l * per) * 16));
+    for (int m = 0; m < msgs; ++m) {
+      const int sl0 = (first + m * stride) * G, n = slices(m);
+      int l = sl0 / per, k = sl0 - l * per;
+      for (int s = 0; s < n; ++s) {          // once per adapter: G slices of one are 32 G bytes of a row
+        if (s == 0 || k == 0)
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(brow + ls.id[ls.list[l]] * b_pitch + k * 16));
+        if (++k == per) { k = 0; ++l; }
       }
+    }
   ready();
   struct Set { uint4 v[G][2], b[G][2]; };
   Set set[2];

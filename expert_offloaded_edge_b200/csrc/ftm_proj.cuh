@@ -142,6 +142,8 @@ __global__ void __launch_bounds__(kProjThreads, 1) proj_kernel(const __grid_cons
     __syncwarp();
   } else if (warp == 1) {
     if (lane == 0) {
+      // the bounded waits begin when what they wait for may: not while an earlier launch still runs
+      if (!LORA && a.early < 2) pdl_wait();
       const bool amn = a.a_mn;
       const uint32_t idesc = kIdesc | (amn ? 1u << 15 : 0u);
       int stage = 0;
@@ -178,6 +180,7 @@ __global__ void __launch_bounds__(kProjThreads, 1) proj_kernel(const __grid_cons
     __syncwarp();
   } else {
     bool ok = true;
+    if (!LORA && a.early < 2) pdl_wait();
     if constexpr (LORA) {
       const int e = threadIdx.x - 64;
       const int i0 = e < BN ? lora_id(a.lora.ids, a.T, a.lora.n, n0 + e) : -1;
