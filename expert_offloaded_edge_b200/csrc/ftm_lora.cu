@@ -95,22 +95,37 @@ __device__ __forceinline__ int shrink_tile(const ShrinkArgs& p, ShrinkTile<MT>& 
   for (int t = threadIdx.x; t + 1 < Tw; t += kShrinkThreads)
     changes += s.key[t] / kShrinkWindow != s.key[t + 1] / kShrinkWindow;
   const bool mixed = Tw > MT && __syncthreads_count(changes) * 16 > Tw;
-  for (int t = threadIdx.x; t < Tw; t += kShrinkThreads) {
-    const uint32_t me = s.key[t];
-    int place = mixed ? 0 : t;
-    if (mixed) {
+  // this thread's two tokens at once
+  static_assert(kShrinkWindow == 2 * kShrinkThreads, "two tokens per thread");
+  const int t0 = threadIdx.x, t1 = t0 + kShrinkThreads;
+  const uint32_t me0 = t0 < Tw ? s.key[t0] : 0u, me1 = t1 < Tw ? s.key[t1] : 0u;
+  int place0 = t0, place1 = t1;
+  if (mixed) {
+    place0 = place1 = 0;
+    if (Tw > kShrinkThreads) {
 #pragma unroll 8
       for (int o = 0; o < Tp; o += 4) {
         const uint4 k = *reinterpret_cast<const uint4*>(&s.key[o]);
-        place += (k.x < me) + (k.y < me) + (k.z < me) + (k.w < me);
+        place0 += (k.x < me0) + (k.y < me0) + (k.z < me0) + (k.w < me0);
+        place1 += (k.x < me1) + (k.y < me1) + (k.z < me1) + (k.w < me1);
+      }
+    } else {
+#pragma unroll 8
+      for (int o = 0; o < Tp; o += 4) {
+        const uint4 k = *reinterpret_cast<const uint4*>(&s.key[o]);
+        place0 += (k.x < me0) + (k.y < me0) + (k.z < me0) + (k.w < me0);
       }
     }
-    if (place >= m0 && place < m0 + MT) {
+  }
+  auto put = [&](int t, uint32_t me, int place) {
+    if (t < Tw && place >= m0 && place < m0 + MT) {
       const int id = static_cast<int>(me / kShrinkWindow);
       s.id[place - m0] = id < p.n ? id : -1;
       s.tok[place - m0] = base + t;
     }
-  }
+  };
+  put(t0, me0, place0);
+  put(t1, me1, place1);
   __syncthreads();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int i = threadIdx.x;
