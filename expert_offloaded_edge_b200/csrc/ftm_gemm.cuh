@@ -21,12 +21,12 @@ __device__ __forceinline__ float silu(float z) { return __fdividef(z, 1.f + __ex
 //   SiLU: q = z.   GELU (tanh form): (1 + tanh(w)) / 2 = sigmoid(2 w), so
 //   q = 2 sqrt(2/pi) (z + 0.044715 z^3).
 // The GELU argument is clamped to [-12, 12], where s is 0 or 1 to fp32, so the
-// cube cannot overflow into 0 * inf.
+// cube cannot overflow into 0 * inf; a NaN passes.
 __device__ __forceinline__ void act_parts(float z, int act, float& s, float& zq) {
   float q = z;
   zq = z;
   if (act == FTM_ACT_GELU_TANH) {
-    const float c = fminf(fmaxf(z, -12.f), 12.f);
+    const float c = z > 12.f ? 12.f : z < -12.f ? -12.f : z;
     const float c2 = c * c;
     q = 1.5957691216057308f * c * fmaf(0.044715f, c2, 1.f);
     zq = 1.5957691216057308f * c * fmaf(0.134145f, c2, 1.f);

@@ -187,6 +187,23 @@ def test_far_values_of_the_activation(act):
         du.assert_within(b.dx[:T], want, bound + du.U * want.abs(), "dx")
 
 
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+@pytest.mark.parametrize("T", [6, 140, 900])
+def test_a_nan_that_was_kept_reaches_the_gradients(T, act):
+    b = Block(T, 256, 640, act, seed=23)
+    b.forward()
+    b.pre[T // 2, 77] = float("nan")
+    b.backward()
+    b.done()
+    n = 2 * b.I * b.d
+    dwg = b.dbank[:n // 2].view(b.I, b.d).isnan()
+    assert bool(dwg[77].all()) and int(dwg.sum()) == b.d
+    dwd = b.dbank[n:n + n // 2].view(b.d, b.I).isnan()
+    assert bool(dwd[:, 77].all()) and int(dwd.sum()) == b.d
+    dx = b.dx[:T].isnan()
+    assert bool(dx[T // 2].all()) and int(dx.sum()) == b.d
+
+
 @pytest.mark.parametrize("T", [9, 300, 1500])
 def test_the_same_call_gives_the_same_bits(T):
     b = Block(T, 640, 384)
