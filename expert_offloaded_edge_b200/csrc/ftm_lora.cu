@@ -28,9 +28,6 @@ namespace ftm {
 // value of x, far below the tensor rate, and takes any mixture of adapters
 // without a layout.
 // ---------------------------------------------------------------------------
-// Weights up to this size are asked into L2 ahead of their use (half of the 126 MB).
-constexpr size_t kPrefetchBytes = 64u << 20;
-
 constexpr int kShrinkThreads = 256;
 constexpr int kShrinkWindow = 512;
 
@@ -43,8 +40,6 @@ struct ShrinkArgs {
   const int32_t* ids;
   int n, rank, rp;
   uint16_t* v;
-  const uint8_t* w;         // the projection's weights, prefetched (w_bytes 0: not wanted)
-  size_t w_bytes;
 };
 
 __device__ __forceinline__ void mma_bf16_16816(float* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -70,16 +65,6 @@ struct ShrinkTile {
 // barrier of the cluster.
 template <int MT>
 __device__ __forceinline__ int shrink_tile(const ShrinkArgs& p, ShrinkTile<MT>& s, int base, int m0, int ks) {
-  // The projection's weights into L2 while v is computed, every block its share.
-  if (p.w_bytes && threadIdx.x == 0) {
-    const size_t blocks = static_cast<size_t>(gridDim.x) * gridDim.y, b = static_cast<size_t>(blockIdx.y) * gridDim.x + blockIdx.x;
-    const size_t share = ((p.w_bytes + blocks - 1) / blocks + 15) & ~static_cast<size_t>(15);
-    const size_t lo = b * share, hi = lo + share < p.w_bytes ? lo + share : p.w_bytes;
-    for (size_t at = lo; at < hi; at += 16384) {
-      const uint32_t bytes = static_cast<uint32_t>(hi - at < 16384 ? hi - at : 16384);
-      asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p.w + at), "r"(bytes) : "memory");
-    }
-  }
   pdl_wait();
   pdl_trigger();
   // Every adapter (n for none) and token of the window make one key.  Where the ids change often (a mixed
@@ -481,9 +466,7 @@ const char* launch_lora(const LoraCall& c, cudaStream_t st, cudaError_t* cerr) {
   const bool pairs = !proj_fits(c.T, c.d_out, 128);
 
   // v first
-  const size_t wb = 2ull * c.d_in * c.d_out;
-  const ShrinkArgs p = {c.x, c.ldx, c.T, c.d_in, c.a, c.scale, c.ids, c.n, c.rank, rp, c.v,
-                        reinterpret_cast<const uint8_t*>(c.w), wb <= kPrefetchBytes && c.T <= kShrinkWindow ? wb : 0};
+  const ShrinkArgs p = {c.x, c.ldx, c.T, c.d_in, c.a, c.scale, c.ids, c.n, c.rank, rp, c.v};
   *cerr = launch_shrink_for(p, st);
   if (*cerr != cudaSuccess) return "adapter shrink launch failed";
 
