@@ -1,12 +1,14 @@
 // The shared projection with low-rank adapters of many requests:
 //   y[t] = x[t] W^T + s[a] (x[t] A[a]^T) B[a]^T
-// in two launches, the second started early (programmatic dependent launch):
+// a handful of tokens in one launch (ftm_lora_token.cuh), others in two, the
+// second started early (programmatic dependent launch):
 //   1. lora_shrink_kernel: v[t] = s[a] (x[t] A[a]^T), rounded to bf16 (the
-//      operand type of the second product; a relative 2^-9 of the adapter's
+//      operand type of the second product; at most 2^-8 of the adapter's
 //      part of y alone);
 //   2. the projection over K = d_in and the adapters' K range (ftm_lora.cuh):
 //      ftm_proj.cuh for few tokens (bound by the bytes of W), the CTA-pair
 //      engine of ftm_dense.cuh for many.
+#include "ftm_lora_token.cuh"
 #include "ftm_proj.cuh"
 
 namespace ftm {
@@ -41,15 +43,6 @@ struct ShrinkArgs {
   int n, rank, rp;
   uint16_t* v;
 };
-
-__device__ __forceinline__ void mma_bf16_16816(float* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                               uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, "
-      "%3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
 
 // A block's tile: the tokens in its places and the distinct adapters among them.
 template <int MT>
@@ -463,6 +456,12 @@ static cudaError_t launch_shrink_for(const ShrinkArgs& p, cudaStream_t st) {
 const char* launch_lora(const LoraCall& c, cudaStream_t st, cudaError_t* cerr) {
   const int rp = (c.rank + 15) / 16 * 16;
   *cerr = cudaSuccess;
+  const TokenArgs few = {c.x, c.w, c.a, c.b, c.scale, c.ids, c.y, c.ldx, c.ldy, c.T, c.d_in, c.d_out, c.n, c.rank};
+  int cluster = 0;
+  if (lora_token_fits(few, cluster)) {
+    *cerr = launch_lora_token(few, cluster, st);
+    return *cerr == cudaSuccess ? nullptr : "adapter projection launch failed";
+  }
   const bool pairs = !proj_fits(c.T, c.d_out, 128);
 
   // v first

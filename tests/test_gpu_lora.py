@@ -77,6 +77,79 @@ def test_projection(T, d_in, d_out, n, rank, mix):
     m.check()
 
 
+@pytest.mark.parametrize("T,d_in,d_out,n,rank,mix", [
+    # a handful of tokens: one launch up to 8 tokens and 8 groups of 16 adapter rows, in clusters of 4 or 8; beyond, two
+    (1, 24, 40, 2, 128, "one"), (1, 6144, 264, 3, 72, "one"), (3, 8, 136, 3, 16, "none"), (4, 4096, 1000, 9, 16, "distinct"),
+    (4, 200, 520, 9, 32, "distinct"), (4, 72, 128, 9, 40, "distinct"), (5, 1032, 16, 5, 8, "distinct"),
+    (7, 328, 248, 3, 16, "mixed"), (8, 136, 72, 8, 16, "distinct"), (8, 512, 2056, 12, 8, "distinct"),
+    (8, 512, 72, 12, 24, "distinct"), (9, 512, 72, 12, 8, "distinct"), (2, 64, 4544, 2, 24, "mixed"),
+    (2, 1024, 4552, 2, 64, "distinct"), (2, 1032, 4552, 2, 64, "distinct"), (6, 264, 8456, 6, 16, "distinct"),
+    (3, 64, 9096, 3, 16, "distinct"), (8, 40, 128, 1, 16, "one")])
+@pytest.mark.parametrize("scaled", [True, False])
+def test_a_handful_of_tokens(T, d_in, d_out, n, rank, mix, scaled):
+    m = Linear(T, d_in, d_out, n, rank, mix, seed=T + rank, scaled=scaled)
+    m.run()
+    m.done()
+    m.check()
+
+
+def test_a_handful_of_tokens_between_two_streams_and_in_a_graph():
+    """Clusters of 4 and 8 in turn, in one graph and on two streams at once."""
+    a, b = Linear(3, 2048, 2048, 5, 16, "distinct", seed=1), Linear(8, 1000, 4104, 8, 16, "distinct", seed=2)
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for m, st in zip((a, b), streams):
+            m.run(st)
+    a.done()
+    a.check()
+    b.check()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        for m in (a, b, a, b):
+            m.run()
+    for m in (a, b):
+        m.x.copy_(normal(9, *m.x.shape))
+        m.ids.copy_(adapters_of(m.T, m.D.n_adapters, "mixed", 4))
+        m.y.fill_(CANARY)
+    g.replay()
+    a.done()
+    a.check()
+    b.check()
+
+
+def test_a_handful_of_tokens_is_isolated_and_strided():
+    T, d_in, d_out = 8, 264, 200
+    m = Linear(T, d_in, d_out, 8, 16, "distinct", seed=3)
+    m.ids[1], m.ids[5] = m.ids[0], -1
+    big = torch.full((T + 2, d_in + d_out + 48), CANARY, dtype=torch.bfloat16, device="cuda")
+    x, y = big[:T, 16:16 + d_in], big[:T, d_in + 32:d_in + 32 + d_out]
+    x.copy_(m.x)
+    before = big.clone()
+
+    def run():
+        ftm.ftm_lora_linear(m.D, x, T, m.w, m.a, m.b, m.scale, m.ids, y, m.ws, m.ws.numel(), ldx=big.stride(0),
+                            ldy=big.stride(0))
+        m.done()
+    run()
+    want, bound = du.lora(m.x, m.w, m.a, m.b, m.scale, m.ids)
+    du.assert_within(y, want, bound, "y")
+    before[:T, d_in + 32:d_in + 32 + d_out] = y
+    assert torch.equal(big, before)
+    clean = y.clone()
+    a2, a3, a4 = (int(m.ids[t]) for t in (2, 3, 4))
+    m.a[a2, 3, 7], m.b[a3, ::5, 2], m.scale[a4] = float("nan"), float("inf"), float("nan")
+    x[6, 1] = float("inf")
+    run()
+    broken = torch.tensor([t in (2, 3, 4, 6) for t in range(T)], device="cuda")
+    broken |= torch.isin(m.ids, m.ids[torch.tensor([2, 3, 4], device="cuda")])
+    assert torch.equal(y[~broken], clean[~broken])
+    assert bool(y[2].isnan().all()) and bool(y[4].isnan().all()) and not bool(torch.isfinite(y[6]).any())
+    assert not bool(torch.isfinite(y[3, ::5]).any())
+    own = torch.arange(d_out, device="cuda") % 5 != 0
+    assert torch.equal(y[3, own], clean[3, own])
+
+
 @pytest.mark.parametrize("T", [12, 600])
 def test_without_scales(T):
     m = Linear(T, 256, 4096, 5, 16, scaled=False)
