@@ -13,10 +13,11 @@
 // dg, du and h are rounded to bf16 between the two backward launches, as the
 // operands of the next products; every sum is fp32.
 //
-// Each product runs on one of two engines: tiles of 256 x 256 on CTA pairs
-// (ftm_dense.cuh), or, for few tokens, 128 rows of weights at a time
-// (ftm_proj.cuh).
+// Each product runs on one of three engines: tiles of 256 x 256 on CTA pairs
+// (ftm_dense.cuh), for few tokens 128 rows of weights at a time (ftm_proj.cuh),
+// and for a handful 16 rows from registers (ftm_token.cuh).
 #include "ftm_proj.cuh"
+#include "ftm_token.cuh"
 
 namespace ftm {
 
@@ -29,7 +30,12 @@ const char* launch_gated_ffn(int act, const void* x, int T, int d, int I, const 
   const uint64_t rd = 2ull * d, rI = 2ull * I;          // bytes of a row
   *cerr = cudaSuccess;
   prof_mark(FTM_K_GEMM1, st, false);
-  if (proj_fits(T, I, 64)) {
+  const TokenProduct gate_up = {static_cast<const uint16_t*>(bank), static_cast<const uint16_t*>(x),
+                                static_cast<uint16_t*>(h), static_cast<uint16_t*>(pre), T, d, I, act, 0};
+  const bool handful = token_fits(T, d, I);
+  if (handful) {
+    *cerr = launch_token_product<true>(gate_up, st);
+  } else if (proj_fits(T, I, 64)) {
     ProjArgs g = {};
     g.T = T;
     g.M = I;
@@ -58,7 +64,11 @@ const char* launch_gated_ffn(int act, const void* x, int T, int d, int I, const 
   prof_mark(FTM_K_GEMM1, st, true);
   if (*cerr != cudaSuccess) return "gate/up launch failed";
   prof_mark(FTM_K_GEMM2, st, false);
-  if (proj_fits(T, d, 128)) {
+  const TokenProduct down = {reinterpret_cast<const uint16_t*>(w + w_d_off), static_cast<const uint16_t*>(h),
+                             static_cast<uint16_t*>(y), nullptr, T, I, d, act, 1};
+  if (handful) {
+    *cerr = launch_token_product<false>(down, st);
+  } else if (proj_fits(T, d, 128)) {
     ProjArgs g = {};
     g.T = T;
     g.M = d;

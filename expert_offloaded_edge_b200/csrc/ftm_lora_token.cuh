@@ -8,24 +8,15 @@
 // without a second launch, and A is read once per cluster.  A CTA then adds
 // B[a] v of its own outputs, a token's own adapter only, in fp32.
 //
-// mma.sync with 16 rows of weights on the M side and the tokens on the N side,
-// fed from registers: bound by the latency of W's bytes, which needs many loads
-// in flight and no layout.  Each thread loads 16 consecutive bytes of a row per
-// operand; the depths of one 32-deep step are dealt to the two MMAs in the same
-// order on both sides.  Two blocks of 64 registers a thread per SM: four steps
-// at a time, or one block per SM with room for eight, took 1 token of 2048 to
-// 2048 from 4.8 us to 5.4 and 6.5; asking W into L2 first, to 5.0; all warps at W
-// and then at A, to 5.5.
+// The products are those of ftm_token.cuh.  (Asking W into L2 first: 5.0 us for
+// one token of 2048 to 2048, 4.8 without; all warps at W and then at A: 5.5.)
 #pragma once
 
-#include "ftm_dense.cuh"
+#include "ftm_token.cuh"
 
 namespace ftm {
 
-constexpr int kTokens = 8;                               // at most
-constexpr int kTokenThreads = 512, kTokenWarps = 8;      // warps of each half
-constexpr int kTokenRows = 16;                           // outputs of a CTA
-
+constexpr int kTokenHalf = kTokenThreads / 64;           // warps at W, and at A
 
 struct TokenArgs {
   const uint16_t *x, *w, *a_pool, *b_pool;
@@ -37,57 +28,33 @@ struct TokenArgs {
 };
 
 __global__ void __launch_bounds__(kTokenThreads, 2) lora_token_kernel(const TokenArgs p) {
-  constexpr int kPitch = 20;                             // of a token's 16 sums: a quad's stores fall into different banks
-  constexpr int kLanes = kTokenThreads / (16 * kTokens); // threads of an output at the end
-  __shared__ float red[2][kTokenWarps][kTokens * kPitch];   // [half][warp][token][row]
-  __shared__ __align__(16) uint16_t s_v[kTokens][128];
-  const int lane = threadIdx.x % 32, half = threadIdx.x / 32 / kTokenWarps, warp = threadIdx.x / 32 % kTokenWarps;
-  const int g = lane >> 2, tq = lane & 3;
+  constexpr int kLanes = kTokenThreads / (kTokenRows * kTokenTile);     // threads of an output at the end
+  __shared__ float red[2][kTokenHalf][kTokenTile * kTokenPitch];        // [half][warp][token][row]
+  __shared__ __align__(16) uint16_t s_v[kTokenTile][128];
+  const int lane = threadIdx.x % 32, half = threadIdx.x / 32 / kTokenHalf, warp = threadIdx.x / 32 % kTokenHalf;
+  const int g = lane >> 2;
   const int m0 = blockIdx.x * kTokenRows;
   const int nc = static_cast<int>(cluster_nranks());
   asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
   pdl_wait();
   pdl_trigger();
 
-  const int steps = (p.K + 31) / 32;
-  const uint16_t* xr = g < p.T ? p.x + g * p.ldx : nullptr;
-  // this warp's share of K of 16 rows (r0, r1: this thread's two) and the tokens, into `to`
-  auto dot = [&](const uint16_t* r0, const uint16_t* r1, float* to) {
-    constexpr int U = 2;
-    const uint4 zero = make_uint4(0, 0, 0, 0);
-    float acc[4] = {};
-    // two neighbouring steps (128 bytes of a row) are a warp's, then the next warp's
-    for (int c = U * warp; c < steps; c += kTokenWarps * U) {
-      uint4 a0[U], a1[U], b[U];
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int k = (c + u) * 32 + tq * 8;
-        const bool in = k < p.K;
-        a0[u] = in && r0 ? __ldg(reinterpret_cast<const uint4*>(r0 + k)) : zero;
-        a1[u] = in && r1 ? __ldg(reinterpret_cast<const uint4*>(r1 + k)) : zero;
-        b[u] = in && xr ? __ldg(reinterpret_cast<const uint4*>(xr + k)) : zero;
-      }
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        mma_bf16_16816(acc, a0[u].x, a1[u].x, a0[u].y, a1[u].y, b[u].x, b[u].y);
-        mma_bf16_16816(acc, a0[u].z, a1[u].z, a0[u].w, a1[u].w, b[u].z, b[u].w);
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) to[(2 * tq + (i & 1)) * kPitch + (i >> 1) * 8 + g] = acc[i];
+  const uint16_t* const xr[1] = {g < p.T ? p.x + g * p.ldx : nullptr};
+  auto dot = [&](const uint16_t* r0, const uint16_t* r1) {
+    token_dot<1>(r0, r1, xr, p.K, warp, kTokenHalf, red[half][warp], [] {});
   };
   auto sum = [&](int h, int t, int row) {
     float f = 0.f;
 #pragma unroll
-    for (int w = 0; w < kTokenWarps; ++w) f += red[h][w][t * kPitch + row];
+    for (int w = 0; w < kTokenHalf; ++w) f += red[h][w][t * kTokenPitch + row];
     return f;
   };
 
-  const int id = lane < kTokens ? lora_id(p.ids, p.T, p.n, lane) : -1;      // of token `lane`
+  const int id = lane < kTokenTile ? lora_id(p.ids, p.T, p.n, lane) : -1;      // of token `lane`
   if (half == 0) {
     const int r = m0 + g;
     dot(r < p.M ? p.w + static_cast<size_t>(r) * p.K : nullptr,
-        r + 8 < p.M ? p.w + static_cast<size_t>(r + 8) * p.K : nullptr, red[0][warp]);
+        r + 8 < p.M ? p.w + static_cast<size_t>(r + 8) * p.K : nullptr);
     asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
   } else {
     asm volatile("barrier.cluster.wait.aligned;" ::: "memory");   // every CTA runs: its s_v may be written
@@ -99,7 +66,7 @@ __global__ void __launch_bounds__(kTokenThreads, 2) lora_token_kernel(const Toke
       const int aid = __shfl_sync(0xffffffffu, id, __fns(heads, 0, li + 1));
       const uint16_t* A = p.a_pool + (static_cast<size_t>(aid) * p.rank + n0) * p.K;
       dot(n0 + g < p.rank ? A + static_cast<size_t>(g) * p.K : nullptr,
-          n0 + g + 8 < p.rank ? A + static_cast<size_t>(g + 8) * p.K : nullptr, red[1][warp]);
+          n0 + g + 8 < p.rank ? A + static_cast<size_t>(g + 8) * p.K : nullptr);
       asm volatile("bar.sync 1, 256;" ::: "memory");
       // a warp of the first four takes two tokens
       const int t = warp * 2 + (lane >> 4), row = lane & 15;
@@ -150,14 +117,14 @@ __global__ void __launch_bounds__(kTokenThreads, 2) lora_token_kernel(const Toke
 // two launches of ftm_lora.cu:
 //   1 token,  2048 -> 2048, rank 8      4.3   7.4 us
 //   1 token,  4096 -> 4096, rank 16     9.6  13.1
-//   4 tokens, 4096 -> 4096, rank 16    10.6  13.8
+//   4 tokens, 4096 -> 4096, rank 16    11.1  13.8
 //   8 tokens, 2048 -> 2048, rank 16     6.8   8.2
 //   8 tokens, 4096 -> 4096, rank 16    14.2  14.3   (two passes of a cluster of 4: 16.6)
 //   2 tokens, 1024 -> 6144, rank 32     8.0   8.4   (two waves)
 //   2 tokens, 4096 -> 6144, rank 64    19.2  17.0   (two waves, not taken)
 inline bool lora_token_fits(const TokenArgs& p, int& cluster) {
   const int groups = p.T * ((p.rank + 15) / 16);
-  if (p.T > kTokens || groups > 8) return false;
+  if (p.T > kTokenTile || groups > 8) return false;
   cluster = groups <= 4 ? 4 : 8;          // of 8: fewer fit beside one another
   struct Fit { int n[2]; };
   static const Fit fit = [] {

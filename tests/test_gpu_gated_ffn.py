@@ -111,6 +111,48 @@ def test_model_widths_and_deep_sums(T, d, I):
     b.check_backward()
 
 
+# a handful of tokens: one and two tiles of 8, K below and above a pass of the warps, and (16 tokens) weights too large
+@pytest.mark.parametrize("T,d,I", [(3, 128, 1152), (7, 1152, 128), (8, 384, 256), (9, 256, 384), (15, 128, 128), (12, 4096, 1024),
+                                   (16, 6144, 2048)])
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+def test_a_handful_of_tokens(T, d, I, act):
+    b = Block(T, d, I, act, seed=T)
+    b.forward(pre=False)
+    b.done()
+    b.check_forward(pre=False)
+    first = b.y.clone()
+    b.forward()
+    b.done()
+    b.check_forward()
+    assert torch.equal(b.y, first)
+    b.backward()
+    b.done()
+    b.check_backward()
+
+
+def test_a_handful_of_tokens_captured_and_chained():
+    """Blocks one behind the other, each reading what the one before wrote, in one graph: every launch starts early."""
+    T, d = 6, 512
+    blocks = [Block(T, d, I, "silu", seed=I) for I in (128, 1024, 384, 640)]
+    bare = [b.y[:T] for b in blocks]
+    for b, y in zip(blocks[1:], bare):
+        b.x = y
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        for _ in range(3):
+            for b in blocks:
+                b.forward()
+    for seed in range(4):
+        blocks[0].x.copy_(normal(seed, T, d))
+        for b in blocks:
+            b.y[:T].fill_(float("nan"))
+        g.replay()
+        for b in blocks:
+            b.done()
+            b.check_forward()
+
+
 @pytest.mark.parametrize("T", [5, 200, 1100])
 def test_inference_keeps_nothing_and_answers_the_same(T):
     b = Block(T, 512, 256)
