@@ -25,8 +25,6 @@
 
 namespace ftm {
 
-constexpr int kProjThreads = 192;   // warp 0 TMA, warp 1 MMA, warps 2-5 adapters' feed and accumulator drain
-
 struct ProjArgs {
   CUtensorMap a, x;        // weights (boxes of 64 rows x 64 deep, either majorness), tokens {K, T}
   int T, M, kb;            // tokens, outputs, 64-deep blocks
@@ -51,6 +49,13 @@ struct ProjShape {
   static constexpr uint32_t kBuf = LORA ? 128 * 32 + BN * 32 : 0;      // a slice of B[a] and one of v
   static constexpr uint32_t kRed = BN * 512 + 8 * 64;                  // partial sums of every rank, each rounded up
   static constexpr uint32_t kTmemCols = BN < 32 ? 32 : BN;
+  // warp 0 TMA, warp 1 MMA, then the warps that drain the accumulator and write the outputs, the first four also the
+  // adapters' feed.  Sixteen for 128 tokens, a quadrant's four with 32 columns each: there the drain and the outputs
+  // take longer than the MMAs (on four warps 333 tokens x 768 outputs, 2048 deep, 1.8 us of MMAs, 2 and 2; a training
+  // step of 333 tokens 41.3 us, 40.1 on eight, 37.6 on sixteen).  Not for 64 tokens, nor with LORA: their registers
+  // leave room for a second block (50 tokens, 4096 x 2048, on eight: 61 -> 66 us).
+  static constexpr int kDrain = BN == 128 && !LORA ? 16 : 4;
+  static constexpr int kThreads = 64 + 32 * kDrain;
   static constexpr size_t kSmem = 1024 + static_cast<size_t>(kStages) * kStage + kLoraRing * kGroup * kBuf + kRed;
 };
 
@@ -63,8 +68,10 @@ __device__ __forceinline__ void st_cluster_f32x4(uint32_t addr, const float* f) 
 }
 
 template <int EPI, int BN, bool LORA>
-__global__ void __launch_bounds__(kProjThreads, LORA ? 2 : 1) proj_kernel(const __grid_constant__ ProjArgs a) {
+__global__ void __launch_bounds__(ProjShape<BN, LORA>::kThreads, LORA ? 2 : 1)
+    proj_kernel(const __grid_constant__ ProjArgs a) {
   using S = ProjShape<BN, LORA>;
+  constexpr int kProjThreads = S::kThreads;
   constexpr uint32_t kIdesc = idesc_bf16_f32(128, BN);
   constexpr int kRows = EPI == kEpiGated ? 64 : 128;      // outputs per tile
   constexpr int kPairs = kRows / 2;                       // pieces (2 outputs, 4 tokens) of 4 tokens
@@ -215,10 +222,11 @@ __global__ void __launch_bounds__(kProjThreads, LORA ? 2 : 1) proj_kernel(const 
       const uint32_t tb = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
       // piece (tokens 4 g .. 4 g + 3, outputs of this row's pair): its owner and its place there
       const uint32_t mine = smem_u32(red) + (kr * kParts + er / kRows) * share * 32 + (er & 1) * 16;
-      int local = (er % kRows) / 2, owner = 0;
-      constexpr int kStep = BN < 32 ? BN : 32;
+      constexpr int kStep = BN < 32 ? BN : 32, kTurns = S::kDrain / 4;
+      const int turn = (warp - 2) / 4;
+      int local = (er % kRows) / 2 + turn * (kStep / 4) * kPairs, owner = 0;
 #pragma unroll 1
-      for (int c0 = 0; c0 < valid; c0 += kStep) {
+      for (int c0 = turn * kStep; c0 < valid; c0 += kTurns * kStep) {
         float f[kStep];
 #pragma unroll
         for (int j = 0; j < kStep; j += 16) tmem_ld16(tb + c0 + j, f + j);
@@ -231,6 +239,7 @@ __global__ void __launch_bounds__(kProjThreads, LORA ? 2 : 1) proj_kernel(const 
             local += kPairs;
           }
         }
+        local += (kTurns - 1) * (kStep / 4) * kPairs;
       }
     }
   }
@@ -338,7 +347,7 @@ cudaError_t launch_proj_bn(const ProjArgs& a, cudaStream_t st) {
   cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(S::kSmem));
   if (err != cudaSuccess) return err;
   cudaLaunchConfig_t cfg = {};
-  cfg.blockDim = dim3(kProjThreads);
+  cfg.blockDim = dim3(S::kThreads);
   cfg.dynamicSmemBytes = S::kSmem;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
