@@ -35,7 +35,7 @@ const char* launch_gated_ffn(int act, const void* x, int T, int d, int I, const 
   const bool handful = token_fits(T, d, I);
   if (handful) {
     *cerr = launch_token_product<true>(gate_up, st);
-  } else if (proj_fits(T, I, 64)) {
+  } else if (proj_fits(T, I, 64, d)) {
     ProjArgs g = {};
     g.T = T;
     g.M = I;
@@ -68,7 +68,7 @@ const char* launch_gated_ffn(int act, const void* x, int T, int d, int I, const 
                              static_cast<uint16_t*>(y), nullptr, T, I, d, act, 1};
   if (handful) {
     *cerr = launch_token_product<false>(down, st);
-  } else if (proj_fits(T, d, 128)) {
+  } else if (proj_fits(T, d, 128, I)) {
     ProjArgs g = {};
     g.T = T;
     g.M = d;
@@ -99,7 +99,7 @@ const char* launch_gated_ffn_backward(int act, const void* x, int T, int d, int 
   uint8_t* dg = static_cast<uint8_t*>(dgu);
   const uint64_t rd = 2ull * d, rI = 2ull * I;
   *cerr = cudaSuccess;
-  if (proj_fits(T, I, 128)) {
+  if (proj_fits(T, I, 128, d)) {
     ProjArgs g = {};
     g.T = T;
     g.M = I;
@@ -178,7 +178,7 @@ const char* launch_gated_ffn_backward(int act, const void* x, int T, int d, int 
   for (int i = 0; i < 3; ++i) {
     if (!all[i].out || !alone[i]) continue;
     // the first waits for dg, du and h, those behind it for nothing but the end
-    if (i == 2 && proj_fits(T, d, 128)) {
+    if (i == 2 && proj_fits(T, d, 128, 2 * I)) {
       ProjArgs s = {};
       s.T = T;
       s.M = d;

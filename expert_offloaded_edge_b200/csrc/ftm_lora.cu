@@ -462,7 +462,7 @@ const char* launch_lora(const LoraCall& c, cudaStream_t st, cudaError_t* cerr) {
     *cerr = launch_lora_token(few, cluster, st);
     return *cerr == cudaSuccess ? nullptr : "adapter projection launch failed";
   }
-  const bool pairs = !proj_fits(c.T, c.d_out, 128);
+  const bool pairs = !proj_fits(c.T, c.d_out, 128, c.d_in, true);
 
   // v first
   const ShrinkArgs p = {c.x, c.ldx, c.T, c.d_in, c.a, c.scale, c.ids, c.n, c.rank, rp, c.v};

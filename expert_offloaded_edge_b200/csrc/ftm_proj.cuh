@@ -396,14 +396,19 @@ cudaError_t launch_proj(const ProjArgs& a, cudaStream_t st) {
   }
 }
 
-// Whether a product of T tokens and M outputs (`rows` of them to a tile) runs
-// here: while its tiles leave room for a split over at least two CTAs each.
-// Beyond, the pair engine does four times the products in an MMA of the same
-// time and reads half as much from L2 for each: 512 tokens x 4096 outputs x 4096
-// take 45 us here, 33 there; 200 x 4096 x 2048 takes 10 here, 12 there.
-inline bool proj_fits(int T, int M, int rows) {
+// Whether a product of T tokens and M outputs (`rows` of them to a tile), K
+// deep, runs here: while its tiles leave room for a split over at least two CTAs
+// each, and up to one a CTA where K is short.  Beyond, the pair engine does four
+// times the products in an MMA of the same time and reads half as much from L2
+// for each: 512 tokens x 4096 outputs x 4096 take 45 us here, 33 there; 200 x 4096
+// x 2048 takes 10 here, 12 there.  Between one and two tiles for two CTAs, whole
+// calls: gated blocks of 700 tokens, 2048 x 1024, 25.1 here, 27.0 there; 1000,
+// 1024 x 768, 17.0 and 19.4; 300, 4096 x 2048, 43.8 and 36.7; with adapters (which
+// four warps feed and drain) 700 tokens, 2048 to 2048, 28.1 and 26.8.
+inline bool proj_fits(int T, int M, int rows, int K, bool lora = false) {
   const int bn = proj_tile(T);
-  return static_cast<long>((M + rows - 1) / rows) * ((T + bn - 1) / bn) <= num_sms() / 2;
+  const long tiles = static_cast<long>((M + rows - 1) / rows) * ((T + bn - 1) / bn);
+  return tiles <= num_sms() / 2 || (!lora && K <= 2048 && tiles <= num_sms());
 }
 
 // Maps of the weights [w_rows][K] (a_mn: stored [K][w_rows]) and the tokens [T][K].
