@@ -16,9 +16,9 @@
 //
 // Shared memory stays under half an SM's for BN <= 64, so that the next launch
 // of the chain may move in early and load its weights while this one drains.
-// With LORA, registers (two blocks' share) and shared memory let a block in
-// beside one of the shrink's, to run over x and W while v is computed: 256
-// tokens of 256 requests, 6144 to 2048 at rank 64, 36.0 -> 34.3 us.
+// With LORA, registers (two blocks' share; 103 a thread for 128 tokens) and shared
+// memory let a block in beside one of the shrink's, to run over x and W while v
+// is computed: 256 tokens of 256 requests, 6144 to 2048 at rank 64, 36.0 -> 34.3 us.
 #pragma once
 
 #include "ftm_dense.cuh"
@@ -52,9 +52,11 @@ struct ProjShape {
   // warp 0 TMA, warp 1 MMA, then the warps that drain the accumulator and write the outputs, the first four also the
   // adapters' feed.  Sixteen for 128 tokens, a quadrant's four with 32 columns each: there the drain and the outputs
   // take longer than the MMAs (on four warps 333 tokens x 768 outputs, 2048 deep, 1.8 us of MMAs, 2 and 2; a training
-  // step of 333 tokens 41.3 us, 40.1 on eight, 37.6 on sixteen).  Not for 64 tokens, nor with LORA: their registers
-  // leave room for a second block (50 tokens, 4096 x 2048, on eight: 61 -> 66 us).
-  static constexpr int kDrain = BN == 128 && !LORA ? 16 : 4;
+  // step of 333 tokens 41.3 us, 40.1 on eight, 37.6 on sixteen).  Eight of them with LORA (200 tokens, 2048 to 2048,
+  // 13.8 -> 13.2 us), whose registers still let a block of the shrink in.  Not for 64 tokens: a second block moves in
+  // there (50 tokens, 4096 x 2048, on eight: 61 -> 66 us).
+  static constexpr int kDrain = BN == 128 ? (LORA ? 8 : 16) : 4;
+  static constexpr int kBlocks = LORA && BN < 128 ? 2 : 1;             // that registers are held to
   static constexpr int kThreads = 64 + 32 * kDrain;
   static constexpr size_t kSmem = 1024 + static_cast<size_t>(kStages) * kStage + kLoraRing * kGroup * kBuf + kRed;
 };
@@ -68,7 +70,7 @@ __device__ __forceinline__ void st_cluster_f32x4(uint32_t addr, const float* f) 
 }
 
 template <int EPI, int BN, bool LORA>
-__global__ void __launch_bounds__(ProjShape<BN, LORA>::kThreads, LORA ? 2 : 1)
+__global__ void __launch_bounds__(ProjShape<BN, LORA>::kThreads, ProjShape<BN, LORA>::kBlocks)
     proj_kernel(const __grid_constant__ ProjArgs a) {
   using S = ProjShape<BN, LORA>;
   constexpr int kProjThreads = S::kThreads;
@@ -193,26 +195,28 @@ __global__ void __launch_bounds__(ProjShape<BN, LORA>::kThreads, LORA ? 2 : 1)
     bool ok = true;
     if (!LORA && a.early < 2) pdl_wait();
     if constexpr (LORA) {
-      const int e = threadIdx.x - 64;
-      const int i0 = e < BN ? lora_id(a.lora.ids, a.T, a.lora.n, n0 + e) : -1;
-      int at;
-      const int nl = lora_list<128>(ls, e, i0, -1, 0, at);
-      if (e == 0) {
-        messages = lora_messages(nl, a.lora.rp, S::kGroup, kr, ks);
-        mbar_arrive(&count_bar);
+      if (warp < 6) {
+        const int e = threadIdx.x - 64;
+        const int i0 = e < BN ? lora_id(a.lora.ids, a.T, a.lora.n, n0 + e) : -1;
+        int at;
+        const int nl = lora_list<128>(ls, e, i0, -1, 0, at);
+        if (e == 0) {
+          messages = lora_messages(nl, a.lora.rp, S::kGroup, kr, ks);
+          mbar_arrive(&count_bar);
+        }
+        LoraRing ring;
+        auto ready = [] { pdl_wait(); pdl_trigger(); };
+        auto send = [&](uint32_t slot, uint32_t n, bool, bool bad) {
+          ls.msg[slot] = n;
+          if (bad)      // every rank's epilogue looks at its own flag
+            for (int r = 0; r < ks; ++r)
+              asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(mapa_rank(smem_u32(&ls.poison[0]), r)), "r"(kLoraPoison)
+                           : "memory");
+          mbar_arrive(&ls.full[slot]);
+        };
+        ok = lora_feed<BN, 128, S::kGroup>(a.lora, ls, ring, ext, 128 * 32, 0, S::kBuf, e, nl, kr, ks, n0 + e,
+                                           i0 >= 0 ? at : -1, w0, ready, send);
       }
-      LoraRing ring;
-      auto ready = [] { pdl_wait(); pdl_trigger(); };
-      auto send = [&](uint32_t slot, uint32_t n, bool, bool bad) {
-        ls.msg[slot] = n;
-        if (bad)      // every rank's epilogue looks at its own flag
-          for (int r = 0; r < ks; ++r)
-            asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(mapa_rank(smem_u32(&ls.poison[0]), r)), "r"(kLoraPoison)
-                         : "memory");
-        mbar_arrive(&ls.full[slot]);
-      };
-      ok = lora_feed<BN, 128, S::kGroup>(a.lora, ls, ring, ext, 128 * 32, 0, S::kBuf, e, nl, kr, ks, n0 + e,
-                                         i0 >= 0 ? at : -1, w0, ready, send);
     }
     // this rank's partial sums to the ranks that own them: lane = weight row, TMEM column = token
     const int q = warp % 4, er = q * 32 + lane;
