@@ -16,6 +16,8 @@
 // Each product runs on one of three engines: tiles of 256 x 256 on CTA pairs
 // (ftm_dense.cuh), for few tokens 128 rows of weights at a time (ftm_proj.cuh),
 // and for a handful 16 rows from registers (ftm_token.cuh).
+#include <initializer_list>
+
 #include "ftm_proj.cuh"
 #include "ftm_token.cuh"
 
@@ -163,22 +165,30 @@ const char* launch_gated_ffn_backward(int act, const void* x, int T, int d, int 
       return kMapsFailed;
   }
   const int pairs = num_sms() / 2;
-  DenseArgs g = {};
-  for (int i = 0; i < 3; ++i) {
-    const DenseProblem& Q = problems[i];
-    alone[i] = Q.tiles <= pairs / 2 && Q.kb - work / pairs >= 24;
-    if (all[i].out && !alone[i]) g.p[g.n++] = Q;
-  }
+  for (int i = 0; i < 3; ++i) alone[i] = problems[i].tiles <= pairs / 2 && problems[i].kb - work / pairs >= 24;
+  // In order: split weight gradients, which leave pairs idle for those behind
+  // them, the common launch, a split dx.  The first waits for dg, du and h, those
+  // behind it for nothing but the end.
   bool launched = false;
-  if (g.n) {
-    *cerr = launch_dense<kEpiStore, false>(g, false, st);
-    if (*cerr != cudaSuccess) return "gradient products launch failed";
+  auto launch = [&](std::initializer_list<int> which, bool split) -> cudaError_t {
+    DenseArgs g = {};
+    for (int i : which)
+      if (all[i].out && alone[i] == split) g.p[g.n++] = problems[i];
+    if (!g.n) return cudaSuccess;
+    g.early = launched;
     launched = true;
+    return launch_dense<kEpiStore, false>(g, split, st);
+  };
+  if (alone[0] && alone[1] && problems[0].tiles + problems[1].tiles <= pairs / 2) {
+    *cerr = launch({0, 1}, true);
+  } else {
+    *cerr = launch({0}, true);
+    if (*cerr == cudaSuccess) *cerr = launch({1}, true);
   }
-  for (int i = 0; i < 3; ++i) {
-    if (!all[i].out || !alone[i]) continue;
-    // the first waits for dg, du and h, those behind it for nothing but the end
-    if (i == 2 && proj_fits(T, d, 128, 2 * I)) {
+  if (*cerr == cudaSuccess) *cerr = launch({0, 1, 2}, false);
+  if (*cerr != cudaSuccess) return "gradient products launch failed";
+  if (dx && alone[2]) {
+    if (proj_fits(T, d, 128, 2 * I)) {
       ProjArgs s = {};
       s.T = T;
       s.M = d;
@@ -188,14 +198,9 @@ const char* launch_gated_ffn_backward(int act, const void* x, int T, int d, int 
       if (!proj_maps(s, w, true, d, 2ull * I, rd, dgu, 2 * rI)) return kMapsFailed;
       *cerr = launch_proj<kEpiStore, false>(s, st);
     } else {
-      DenseArgs s = {};
-      s.n = 1;
-      s.p[0] = problems[i];
-      s.early = launched;
-      *cerr = launch_dense<kEpiStore, false>(s, true, st);
+      *cerr = launch({2}, true);
     }
     if (*cerr != cudaSuccess) return "gradient product launch failed";
-    launched = true;
   }
   return nullptr;
 }

@@ -614,7 +614,7 @@ __global__ void __launch_bounds__(DenseShape<EPI, LORA>::kThreads, 1)
           }
         }
       };
-      finish(g.p[0], ti, poison, [] { return true; }, load,
+      finish(g.p[ti.p], ti, poison, [] { return true; }, load,
              [&](int cc) { return SplitUnits<EPI>::owner(EPI == kEpiStore ? 2 * cc : cc, ks) == kr; });
       if (lane == 0) bulk_wait_all();
       __syncwarp();
@@ -711,7 +711,7 @@ cudaError_t launch_dense_split(DenseArgs& a, cudaStream_t st) {
   const int tiles = a.n_long + a.n_short;
   int ks = 1;
   if (SPLIT)
-    for (int c = 2; c <= 4 && c <= a.p[0].kb; ++c)
+    for (int c = 2; c <= 4 && c <= a.p[a.n - 1].kb; ++c)
       if (tiles <= fit.n[c]) ks = c;
   attr[0].val.clusterDim.x = 2 * ks;
   cfg.gridDim = dim3(SPLIT ? 2 * ks * tiles : 2 * (tiles < fit.n[1] ? tiles : fit.n[1]));
@@ -723,7 +723,12 @@ cudaError_t launch_dense_split(DenseArgs& a, cudaStream_t st) {
 // blocks of 64 a pair (an exchange costs as much as 4 blocks).
 template <int EPI, bool LORA>
 cudaError_t launch_dense(DenseArgs& a, bool may_split, cudaStream_t st) {
-  const bool split = may_split && a.n == 1 && a.p[0].tiles <= num_sms() / 4 && a.p[0].kb >= 8;
+  int tiles = 0, kb = 8;
+  for (int i = 0; i < a.n; ++i) {
+    tiles += a.p[i].tiles;
+    kb = a.p[i].kb < kb ? a.p[i].kb : kb;
+  }
+  const bool split = may_split && tiles <= num_sms() / 4 && kb >= 8;
   return split ? launch_dense_split<EPI, LORA, true>(a, st) : launch_dense_split<EPI, LORA, false>(a, st);
 }
 
