@@ -175,6 +175,26 @@ def test_one_of_the_gradients(T, dx, dbank):
     b.check_backward(dx, dbank)
 
 
+@pytest.mark.parametrize("T,d,I", [(5000, 256, 128), (9000, 384, 640), (12983, 768, 128), (333, 512, 1024), (70, 2048, 1920)])
+def test_a_gradient_has_the_same_bits_whichever_others_are_asked_for(T, d, I):
+    """Weight gradients split along K in a launch of their own, and dx behind or beside them."""
+    b = Block(T, d, I, "silu", seed=T)
+    b.forward()
+    b.backward()
+    b.done()
+    b.check_backward()
+    dx, dbank = b.dx.clone(), b.dbank.clone()
+    b.dx.fill_(CANARY)
+    b.dbank.fill_(CANARY)
+    b.backward(dbank=False)
+    b.done()
+    assert torch.equal(b.dx, dx) and bool((b.dbank == CANARY).all())
+    b.dx.fill_(CANARY)
+    b.backward(dx=False)
+    b.done()
+    assert torch.equal(b.dbank, dbank) and bool((b.dx == CANARY).all())
+
+
 def test_no_tokens():
     b = Block(1, 256, 128)
     ftm.ftm_gated_ffn(b.L, 0, None, 0, None, None, None, None, 0)
