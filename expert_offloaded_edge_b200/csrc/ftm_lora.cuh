@@ -11,9 +11,11 @@
 // four warps write to shared memory.
 //
 // A zero row does not mask an infinity or NaN of another request's adapter
-// (0 * inf = NaN).  The feeding threads see every slice of B[a], so they take
-// non-finite weights out of it and flag the tile; the epilogue of a flagged
-// tile adds the exact non-finite terms to the adapter's own tokens only.
+// (0 * inf = NaN).  The feeding threads see every slice of B[a], so they put a
+// tiny weight of the same sign in a non-finite one's place and flag the tile; the
+// epilogue of a flagged tile adds the non-finite terms to the adapter's own tokens
+// only.  (Tiny and not zero: an infinite v times it is the infinity that the term
+// is; a finite v adds next to nothing to what will be infinite or NaN.)
 #pragma once
 
 #include "ftm_gemm.cuh"
@@ -75,9 +77,10 @@ __device__ __forceinline__ uint32_t bf16_pair_nonfinite(uint32_t w) {
 __device__ __forceinline__ uint32_t bf16x8_nonfinite(uint4 w) {
   return bf16_pair_nonfinite(w.x) | bf16_pair_nonfinite(w.y) | bf16_pair_nonfinite(w.z) | bf16_pair_nonfinite(w.w);
 }
+// The smallest normal of the same sign for each infinity and NaN of the pair.
 __device__ __forceinline__ uint32_t bf16_pair_finite(uint32_t w) {
-  if ((w & 0x7f80u) == 0x7f80u) w &= 0xffff0000u;
-  if ((w & 0x7f800000u) == 0x7f800000u) w &= 0xffffu;
+  if ((w & 0x7f80u) == 0x7f80u) w = (w & 0xffff8000u) | 0x0080u;
+  if ((w & 0x7f800000u) == 0x7f800000u) w = (w & 0x8000ffffu) | 0x00800000u;
   return w;
 }
 

@@ -365,3 +365,33 @@ def test_served_block_with_adapters_and_its_training_step(T):
     du.assert_within(dx, wx, ex, "dx")
     du.assert_within(dbank[:2 * I * d].view(2 * I, d), ww, ew, "dw_gu")
     du.assert_within(dbank[2 * I * d:].view(d, I), wd, ed, "dw_d")
+
+
+@pytest.mark.parametrize("T,d_in,d_out", [(4, 264, 256), (7, 264, 256), (24, 264, 256), (100, 256, 4096), (640, 520, 2048), (2500, 264, 2048)])
+def test_an_infinite_low_rank_value_meets_infinite_weights(T, d_in, d_out):
+    """s (x A^T) beyond the largest bf16 is an infinity of its sign; with weights of B that are infinite, and others
+    that are not, of one sign an output is that infinity, of both NaN, on every engine."""
+    m = Linear(T, d_in, d_out, 4, 24, "mixed", seed=5)
+    m.ids[0], m.ids[T - 1] = 2, -1
+    m.x.abs_()
+    m.a[2].abs_()                        # x A^T is above 1 everywhere, times 3e38 beyond the range
+    m.b[2].abs_()
+    m.scale[2] = 3e38
+    inf = float("inf")
+    m.b[2, 0::7, 5] = inf                # outputs 0 mod 7: +inf + (inf * inf); 1 mod 7: -inf everywhere; 2 mod 7: both; others inf * finite
+    m.b[2, 1::7] *= -1
+    m.b[2, 1::7, 23] = -inf
+    m.b[2, 2::7, 3] = -inf
+    m.b[2, 3::7, 9] = float("nan")
+    m.run()
+    m.done()
+    own = m.ids == 2
+    assert bool((m.x[own].double() @ m.a[2].double().T > 2.0).all())
+    got = m.y[:T].double()
+    want = torch.full((d_out,), inf, dtype=torch.float64, device="cuda")
+    want[1::7], want[2::7], want[3::7] = -inf, float("nan"), float("nan")
+    assert torch.equal(got[own].nan_to_num(nan=1.0), want.nan_to_num(nan=1.0).expand(int(own.sum()), d_out))
+    assert torch.equal(got[own].isnan(), want.isnan().expand(int(own.sum()), d_out))
+    ids = torch.where(own, torch.full_like(m.ids, -1), m.ids)
+    ref, bound = du.lora(m.x, m.w, m.a, m.b, m.scale, ids)
+    du.assert_within(got[~own], ref[~own], bound[~own], "other requests")
