@@ -4,7 +4,7 @@
 // second started early (programmatic dependent launch):
 //   1. lora_shrink_kernel: v[t] = s[a] (x[t] A[a]^T), rounded to bf16 (the
 //      operand type of the second product; at most 2^-8 of the adapter's
-//      part of y alone);
+//      part of y alone; one launch keeps it in fp32);
 //   2. the projection over K = d_in and the adapters' K range (ftm_lora.cuh):
 //      ftm_proj.cuh for few tokens (bound by the bytes of W), the CTA-pair
 //      engine of ftm_dense.cuh for many.

@@ -3,10 +3,11 @@
 //
 // Half of a CTA's warps sum its 16 rows of W over all of K, the other half 16
 // rows of the adapters' A: the groups of 16 rows of the adapters that
-// occur are dealt out to the CTAs of a cluster, which hand v = s (x A^T),
-// rounded to bf16, to all of them through shared memory.  So every CTA has v
-// without a second launch, and A is read once per cluster.  A CTA then adds
-// B[a] v of its own outputs, a token's own adapter only, in fp32.
+// occur are dealt out to the CTAs of a cluster, which hand v = s (x A^T) to all
+// of them through shared memory.  So every CTA has v without a second launch, and
+// A is read once per cluster.  A CTA then adds B[a] v of its own outputs, a
+// token's own adapter only, in fp32: v is no tensor-core operand here and is not
+// rounded.
 //
 // The products are those of ftm_token.cuh.  (Asking W into L2 first: 5.0 us for
 // one token of 2048 to 2048, 4.8 without; all warps at W and then at A: 5.5.)
@@ -30,7 +31,7 @@ struct TokenArgs {
 __global__ void __launch_bounds__(kTokenThreads, 2) lora_token_kernel(const TokenArgs p) {
   constexpr int kLanes = kTokenThreads / (kTokenRows * kTokenTile);     // threads of an output at the end
   __shared__ float red[2][kTokenHalf][kTokenTile * kTokenPitch];        // [half][warp][token][row]
-  __shared__ __align__(16) uint16_t s_v[kTokenTile][128];
+  __shared__ __align__(16) float s_v[kTokenTile][128];
   const int lane = threadIdx.x % 32, half = threadIdx.x / 32 / kTokenHalf, warp = threadIdx.x / 32 % kTokenHalf;
   const int g = lane >> 2;
   const int m0 = blockIdx.x * kTokenRows;
@@ -72,11 +73,10 @@ __global__ void __launch_bounds__(kTokenThreads, 2) lora_token_kernel(const Toke
       const int t = warp * 2 + (lane >> 4), row = lane & 15;
       const int mine = __shfl_sync(0xffffffffu, id, t);
       if (t < p.T && mine == aid && n0 + row < p.rank) {
-        const float f = (p.scale ? p.scale[aid] : 1.f) * sum(1, t, row);
-        const uint16_t v = static_cast<uint16_t>(pack_bf16(f, 0.f));
+        const float v = (p.scale ? p.scale[aid] : 1.f) * sum(1, t, row);
         const uint32_t at = smem_u32(&s_v[t][n0 + row]);
         for (int c = 0; c < nc; ++c)
-          asm volatile("st.shared::cluster.u16 [%0], %1;" ::"r"(mapa_rank(at, c)), "h"(v) : "memory");
+          asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(mapa_rank(at, c)), "f"(v) : "memory");
       }
       asm volatile("bar.sync 1, 256;" ::: "memory");              // the sums are read
     }
@@ -98,12 +98,14 @@ __global__ void __launch_bounds__(kTokenThreads, 2) lora_token_kernel(const Toke
   for (int i = 0; i < kPieces; ++i) {
     const int at = sub + i * kLanes;
     if (!low || at >= pieces) break;
-    const uint4 v = *reinterpret_cast<const uint4*>(&s_v[t][at * 8]);
-    const uint32_t vw[4] = {v.x, v.y, v.z, v.w}, bw[4] = {b[i].x, b[i].y, b[i].z, b[i].w};
+    const float4 v0 = *reinterpret_cast<const float4*>(&s_v[t][at * 8]);
+    const float4 v1 = *reinterpret_cast<const float4*>(&s_v[t][at * 8 + 4]);
+    const float v[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+    const uint32_t bw[4] = {b[i].x, b[i].y, b[i].z, b[i].w};
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      f = fmaf(__uint_as_float(vw[j] << 16), __uint_as_float(bw[j] << 16), f);
-      f = fmaf(__uint_as_float(vw[j] & 0xffff0000u), __uint_as_float(bw[j] & 0xffff0000u), f);
+      f = fmaf(v[2 * j], __uint_as_float(bw[j] << 16), f);
+      f = fmaf(v[2 * j + 1], __uint_as_float(bw[j] & 0xffff0000u), f);
     }
   }
 #pragma unroll

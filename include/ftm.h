@@ -542,8 +542,9 @@ typedef struct ftm_lora_desc {
  *               multiple of 8); what lies between the rows is not written.  y
  *               must not overlap an input
  *   workspace   device, >= ftm_lora_workspace_bytes(D, T) bytes, 256-aligned
- * x A^T is summed in fp32, scaled and rounded to bf16; both products are then
- * added in one fp32 accumulator and rounded once.  A token's result depends on
+ * x A^T is summed in fp32, scaled and, but for the few tokens that run in one
+ * launch (up to 8), rounded to bf16 as the second product's operand; both
+ * products are then added in fp32 and rounded once.  A token's result depends on
  * its own row and its own adapter alone: infinities and NaN of other requests'
  * rows or adapters do not reach it.  Deterministic.  T = 0 is a no-op.
  * Pointers, streams, capture and workspaces as ftm_gated_ffn. */

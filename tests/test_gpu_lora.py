@@ -395,3 +395,26 @@ def test_an_infinite_low_rank_value_meets_infinite_weights(T, d_in, d_out):
     ids = torch.where(own, torch.full_like(m.ids, -1), m.ids)
     ref, bound = du.lora(m.x, m.w, m.a, m.b, m.scale, ids)
     du.assert_within(got[~own], ref[~own], bound[~own], "other requests")
+
+
+@pytest.mark.parametrize("T,d_in,d_out,rank,scaled", [(1, 2048, 256, 128, True), (4, 512, 520, 32, False), (8, 264, 136, 16, True)])
+def test_one_launch_rounds_once(T, d_in, d_out, rank, scaled):
+    """Up to 8 tokens in one launch: sums in fp32 from end to end and one rounding, of y.  The adapter's part cancels
+    almost wholly over the rank, so that a rounding of s (x A^T) would be seen."""
+    m = Linear(T, d_in, d_out, T, rank, "distinct", seed=7, scaled=scaled, std=1.0)
+    m.w.zero_()
+    m.a[:, 1::2] = m.a[:, ::2] * 1.0625          # neighbouring values of v: v and 1.0625 v
+    m.a[:, 1::2] = m.a[:, 1::2].to(torch.bfloat16)
+    m.b[:, :, 1::2] = -m.b[:, :, ::2]
+    m.run()
+    m.done()
+    X = m.x.double()
+    A, B = m.a.double()[m.ids.long()], m.b.double()[m.ids.long()]
+    s = torch.ones(T, 1, device="cuda", dtype=torch.float64) if m.scale is None else m.scale.double()[m.ids.long()].unsqueeze(1)
+    v = s * torch.einsum("tk,trk->tr", X, A)
+    want = torch.einsum("tr,tor->to", v, B)
+    # v: sums of K products and a multiplication; y: a sum of rank products and a rounding
+    ev = (du.gamma(d_in) + 2.0 ** -23) * s.abs() * torch.einsum("tk,trk->tr", X.abs(), A.abs())
+    ey = torch.einsum("tr,tor->to", ev + du.gamma(rank) * (v.abs() + ev), B.abs())
+    du.assert_within(m.y[:T], want, ey + du.U * (want.abs() + ey), "y")
+    assert float((want - m.y[:T].double()).norm() / want.norm()) <= du.U      # one rounding's worst case
