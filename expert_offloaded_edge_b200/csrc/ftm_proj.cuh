@@ -12,7 +12,9 @@
 //              out = act(g) * u, and g, u kept on request
 //   kEpiDgate  D = dh: dg, du and h from the kept g and u (A read rows-innermost)
 //   LORA       kEpiStore over K and the adapters' K range (ftm_lora.cuh); the
-//              slices are shared out over the cluster's ranks like K
+//              slices are shared out over the cluster's ranks like K, by their
+//              place in the tile's list of adapters (a token's last bits may
+//              depend on which adapters its tile holds, never on their values)
 //
 // Shared memory stays under half an SM's for BN <= 64, so that the next launch
 // of the chain may move in early and load its weights while this one drains.

@@ -544,9 +544,11 @@ typedef struct ftm_lora_desc {
  *   workspace   device, >= ftm_lora_workspace_bytes(D, T) bytes, 256-aligned
  * x A^T is summed in fp32, scaled and, but for the few tokens that run in one
  * launch (up to 8), rounded to bf16 as the second product's operand; both
- * products are then added in fp32 and rounded once.  A token's result depends on
- * its own row and its own adapter alone: infinities and NaN of other requests'
- * rows or adapters do not reach it.  Deterministic.  T = 0 is a no-op.
+ * products are then added in fp32 and rounded once.  What other
+ * requests' rows and adapters hold, infinities and NaN among it, does not change
+ * a bit of a token's result.  Which adapters the other tokens have, and T, may
+ * change its last bits: they decide which of the partial sums over the depth its
+ * adapter's terms join.  The same call gives the same bits.  T = 0 is a no-op.
  * Pointers, streams, capture and workspaces as ftm_gated_ffn. */
 ftm_status ftm_lora_linear(const ftm_lora_desc* D, const void* x, int64_t ldx, int32_t T, const void* w,
                            const void* lora_a, const void* lora_b, const float* scale, const int32_t* adapter_ids,

@@ -418,3 +418,28 @@ def test_one_launch_rounds_once(T, d_in, d_out, rank, scaled):
     ey = torch.einsum("tr,tor->to", ev + du.gamma(rank) * (v.abs() + ev), B.abs())
     du.assert_within(m.y[:T], want, ey + du.U * (want.abs() + ey), "y")
     assert float((want - m.y[:T].double()).norm() / want.norm()) <= du.U      # one rounding's worst case
+
+
+@pytest.mark.parametrize("T,d_in,d_out,rank", [
+    (6, 264, 200, 16), (24, 320, 256, 40), (60, 1000, 512, 24), (100, 320, 4096, 40), (500, 4096, 2560, 16),
+    (640, 520, 2048, 40), (900, 512, 2048, 16), (2500, 320, 2048, 40)])
+def test_what_other_requests_hold_changes_no_bit(T, d_in, d_out, rank):
+    """With the ids as they are, every other value (rows of other adapters' tokens, the adapters, their scales) may
+    change: a token's bits stay.  One launch, few tokens split along K, CTA pairs split along K (640, 900, 500) and not."""
+    m = Linear(T, d_in, d_out, 6, rank, "mixed", seed=13)
+    m.ids[1] = 3
+    m.run()
+    m.done()
+    m.check()
+    first = m.y.clone()
+    own = m.ids == 3
+    other = torch.arange(6, device="cuda") != 3
+    for seed in (100, 200):
+        m.x[~own] = normal(seed, T, d_in, std=3.0)[~own]
+        m.a[other] = normal(seed + 1, *m.a.shape, std=0.2)[other]
+        m.b[other] = normal(seed + 2, *m.b.shape, std=2.0)[other]
+        m.scale[other] *= -1.7
+        m.run()
+        m.done()
+        m.check()
+        assert torch.equal(m.y[:T][own], first[:T][own]) and not torch.equal(m.y, first)
