@@ -65,7 +65,7 @@ class Linear:
     (16, 256, 128, 16, 16, "distinct"), (17, 256, 264, 4, 40, "mixed"), (33, 1000, 128, 7, 64, "mixed"),
     (64, 512, 1736, 64, 16, "distinct"), (65, 128, 384, 9, 128, "mixed"), (77, 1000, 136, 5, 24, "runs"),
     (128, 320, 1000, 128, 8, "distinct"), (130, 136, 72, 3, 8, "none"), (200, 264, 392, 17, 96, "mixed"),
-    # CTA pairs: split along K, one tile and many to a pair, tiles without adapters, all adapters in every tile
+    # CTA pairs: one tile and many to a pair, tiles without adapters, all adapters in every tile (a tile split along K: SPLIT_PAIRS)
     (300, 1024, 8200, 5, 32, "runs"), (512, 520, 4104, 33, 16, "mixed"), (513, 256, 6152, 4, 48, "runs"),
     (700, 64, 4096, 700, 8, "distinct"), (1100, 1024, 4096, 6, 80, "runs"), (1030, 200, 7000, 3, 112, "one"),
     (2500, 328, 2056, 9, 32, "runs"), (2600, 128, 4096, 12, 64, "mixed"), (5000, 64, 2048, 40, 16, "runs"),
@@ -443,3 +443,91 @@ def test_what_other_requests_hold_changes_no_bit(T, d_in, d_out, rank):
         m.done()
         m.check()
         assert torch.equal(m.y[:T][own], first[:T][own]) and not torch.equal(m.y, first)
+
+
+# CTA pairs, one tile to a cluster whose pairs split the depth: more than 74 tiles of 128 x 128 (else the few-token
+# engine), at most 37 of 256 x 256, d_in >= 512; 20 and 24 tiles in clusters of 3 or 2 pairs, 32 of 2
+SPLIT_PAIRS = [(500, 4096, 2560), (640, 520, 2048), (900, 512, 2048)]
+
+
+@pytest.mark.parametrize("T,d_in,d_out", SPLIT_PAIRS)
+@pytest.mark.parametrize("n,rank,mix", [(6, 40, "mixed"), (3, 128, "runs"), (1, 16, "one"), (4, 64, "none"), (64, 8, "distinct")])
+def test_projection_split_over_pairs(T, d_in, d_out, n, rank, mix):
+    m = Linear(T, d_in, d_out, n, rank, mix, seed=T + rank)
+    outs = []
+    for _ in range(3):
+        m.ws.fill_(255)
+        m.run()
+        m.done()
+        m.check()
+        outs.append(m.y.clone())
+    assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
+
+
+@pytest.mark.parametrize("T,d_in,d_out", SPLIT_PAIRS)
+@pytest.mark.parametrize("broken", range(6))
+def test_requests_are_isolated_where_pairs_split_the_depth(T, d_in, d_out, broken):
+    """One adapter after the other (each lies elsewhere in the tiles' lists, so another pair feeds its slices) has
+    infinities and NaN in B: in every fifth output, so in columns that each of the cluster's pairs finishes."""
+    m = Linear(T, d_in, d_out, 6, 40, "mixed", seed=11)
+    m.run()
+    m.done()
+    clean = m.y.clone()
+    r = (7 * broken) % 40                # a different slice of 16 for different adapters
+    m.b[broken, ::5, r] = float("inf")
+    m.b[broken, 1::5, 39 - r] = float("nan")
+    m.b[broken, 2::5, (r + 16) % 40] = -float("inf")
+    m.run()
+    m.done()
+    own = m.ids == broken
+    assert torch.equal(m.y[:T][~own], clean[:T][~own]) and torch.equal(m.y[T:], clean[T:])
+    got = m.y[:T][own].double()
+    v = (m.x[own].double() @ m.a[broken].double().T) * m.scale[broken].double()
+    ev = (du.gamma(d_in) + 2.0 ** -23) * (m.x[own].double().abs() @ m.a[broken].double().abs().T) * m.scale[broken].double().abs()
+    for at, k, sign in ((0, r, 1.0), (2, (r + 16) % 40, -1.0)):
+        sure = v[:, k].abs() > ev[:, k]                    # the others are zero within the error of their sums
+        assert int(sure.sum()) > 0.9 * sure.numel() and not bool(torch.isfinite(got[:, at::5]).any())
+        far = torch.full_like(got[sure, at::5], sign * float("inf"))
+        assert torch.equal(got[sure, at::5], far * v[sure, k:k + 1].sign())
+    assert bool(got[:, 1::5].isnan().all())
+    finite = torch.arange(d_out, device="cuda") % 5 > 2
+    assert torch.equal(m.y[:T][own][:, finite], clean[:T][own][:, finite])
+
+
+@pytest.mark.parametrize("T,d_in,d_out", SPLIT_PAIRS)
+def test_split_over_pairs_captured_strided_and_on_two_streams(T, d_in, d_out):
+    m = Linear(T, d_in, d_out, 5, 24, "runs", seed=17)
+    big = torch.full((T + 2, d_in + d_out + 48), CANARY, dtype=torch.bfloat16, device="cuda")
+    x, y = big[:T, 16:16 + d_in], big[:T, d_in + 32:d_in + 32 + d_out]
+
+    def run(stream=None):
+        ftm.ftm_lora_linear(m.D, x, T, m.w, m.a, m.b, m.scale, m.ids, y, m.ws, m.ws.numel(), stream, ldx=big.stride(0),
+                            ldy=big.stride(0))
+    x.copy_(m.x)
+    run()
+    m.done()
+    graph, stream = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.stream(stream), torch.cuda.graph(graph, stream=stream):
+        run()
+        run()
+    for mix in ("mixed", "none", "distinct", "runs"):
+        m.ids.copy_(adapters_of(T, 5, mix, seed=2))
+        m.x = normal(78, T, d_in)
+        x.copy_(m.x)
+        before = big.clone()
+        y.fill_(CANARY)
+        graph.replay()
+        m.done()
+        want, bound = du.lora(m.x, m.w, m.a, m.b, m.scale, m.ids)
+        du.assert_within(y, want, bound, "y")
+        before[:T, d_in + 32:d_in + 32 + d_out] = y
+        assert torch.equal(big, before)
+    other = Linear(T + 130, d_in, d_out, 4, 16, "mixed", seed=18)
+    keep, streams = y.clone(), (torch.cuda.Stream(), torch.cuda.Stream())
+    torch.cuda.synchronize()
+    for _ in range(10):
+        run(streams[0])
+        other.run(streams[1])
+    other.done()
+    other.check()
+    assert torch.equal(y, keep)
