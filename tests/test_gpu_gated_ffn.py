@@ -82,7 +82,8 @@ class Block:
             assert bool((self.dbank == CANARY).all())
 
 
-# few tokens (16, 32, 64, 128 to a tile, K split), many (CTA pairs, split and not), ragged in both directions
+# few tokens (16, 32, 64, 128 to a tile, K split), the gradient products on CTA pairs, ragged in both directions (the
+# others on pairs: tests/test_gpu_dense_pairs.py)
 SHAPES = [(1, 128, 128), (2, 256, 128), (16, 128, 384), (17, 384, 256), (33, 256, 128), (64, 640, 128), (65, 128, 640),
           (127, 256, 256), (129, 384, 128), (255, 128, 128), (300, 896, 384), (513, 1024, 896), (700, 2048, 256),
           (1025, 384, 128), (2049, 640, 384)]
