@@ -118,3 +118,14 @@ def assert_within(got, want, bound, what=""):
         i = (~ok).nonzero()[0].tolist()
         raise AssertionError(f"{what}: {int((~ok).sum())} of {ok.numel()} values off; first at {i}: got "
                              f"{float(got[tuple(i)])}, want {float(want[tuple(i)])}, bound {float(bound[tuple(i)]):.3g}")
+
+
+# The relative Frobenius norm of a gradient's error.  A weight gradient's operand (dg, du or h) is rounded once and so
+# is the gradient, each by at most U of a value.  The operand's errors meet the other operand's independent rows, so
+# that over the gradient they add up as the terms themselves do: at most U again, together 2 U.  A fifth more for the
+# fp32 sums (below 2^-23 of the terms' running sum for each 16 of T tokens: 1e-3 at 10^5).
+NORM = 2.4 * U
+
+
+def norm_error(got, want) -> float:
+    return float((f64(got) - want).norm() / want.norm())

@@ -161,3 +161,34 @@ def test_reference_gradients_against_differences(act):
         z = torch.tensor([z0 - 1e-5, z0, z0 + 1e-5], dtype=torch.float64)
         a, s = du.activation(z, act)
         assert abs(float(a[2] - a[0]) / 2e-5 - float(s[1])) < 1e-8
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+def test_the_norm_of_a_gradients_error_sees_a_block_left_out(act):
+    """At 20000 tokens: roundings to bf16 where the kernels make them stay within du.NORM, and 64 tokens that a sum
+    leaves out (its last, or any) do not, in either weight gradient."""
+    g = torch.Generator().manual_seed(5)
+    T, d, I = 20000, 24, 16
+
+    def rand(*s, std=1.0):
+        return (torch.randn(*s, generator=g) * std).to(torch.bfloat16)
+
+    x, bank, dy, pre = rand(T, d), rand(3 * I * d, std=0.2), rand(T, d), rand(T, 2 * I)
+
+    def bf(t):
+        return t.to(torch.bfloat16).double()
+
+    (dx, dw, dwd), _ = du.block_backward(x, bank, pre, dy, d, I, act)
+    wg, wu, wd = du.split_bank(bank, d, I)
+    z, u = pre[:, :I].double(), pre[:, I:].double()
+    a, slope = du.activation(z, act)
+    dh = dy.double() @ wd
+    dgu, h = bf(torch.cat([dh * u * slope, dh * a], 1)), bf(a * u)
+    assert du.norm_error(bf(dgu @ torch.cat([wg, wu])), dx) <= du.NORM
+    assert du.norm_error(bf(dgu.T @ x.double()), dw) <= du.NORM
+    assert du.norm_error(bf(dy.double().T @ h), dwd) <= du.NORM
+    for lost in (slice(T - 64, T), slice(6400, 6464)):
+        keep = torch.ones(T, dtype=torch.bool)
+        keep[lost] = False
+        assert du.norm_error(dgu[keep].T @ x[keep].double(), dw) > 3 * du.NORM
+        assert du.norm_error(dy[keep].double().T @ h[keep], dwd) > 3 * du.NORM

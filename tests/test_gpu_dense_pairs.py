@@ -1,5 +1,5 @@
 """The dense gated block where its products run on CTA pairs (tiles of 256 x 256, with and without a split of the
-depth), and few tokens on wide blocks.  Bounds: tests/dense_util.py."""
+depth), its deep sums, and few tokens on wide blocks.  Bounds: tests/dense_util.py."""
 import pytest
 import torch
 
@@ -159,3 +159,19 @@ def test_few_tokens_on_wide_blocks(T, d, I, act):
     b.done()
     b.check_forward()
     b.check_backward()
+
+
+@pytest.mark.parametrize("T,d,I", [(20000, 256, 128), (12983, 768, 128), (9000, 384, 640), (4100, 256, 1280), (100000, 128, 128)])
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+def test_deep_sums_leave_nothing_out(T, d, I, act):
+    """The worst case's bounds grow with the depth until a block of 64 tokens left out would pass them; the error's
+    norm does not (tests/test_dense_abi.py shows what it sees)."""
+    b = Block(T, d, I, act, seed=T)
+    b.forward()
+    b.backward()
+    b.done()
+    (dx, dw, dwd), _ = du.block_backward(b.x, b.bank, b.pre[:T], b.dy, d, I, act)
+    n = 2 * I * d
+    assert du.norm_error(b.dbank[:n].view(2 * I, d), dw) <= du.NORM
+    assert du.norm_error(b.dbank[n:3 * I * d].view(d, I), dwd) <= du.NORM
+    assert du.norm_error(b.dx[:T], dx) <= du.NORM
