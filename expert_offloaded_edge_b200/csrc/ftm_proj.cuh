@@ -16,11 +16,12 @@
 //              place in the tile's list of adapters (a token's last bits may
 //              depend on which adapters its tile holds, never on their values)
 //
-// Shared memory stays under half an SM's for BN <= 64, so that the next launch
-// of the chain may move in early and load its weights while this one drains.
-// With LORA, registers (two blocks' share; 103 a thread for 128 tokens) and shared
-// memory let a block in beside one of the shrink's, to run over x and W while v
-// is computed: 256 tokens of 256 requests, 6144 to 2048 at rank 64, 36.0 -> 34.3 us.
+// Without LORA, shared memory stays under half an SM's for BN <= 64, so that the
+// next launch of the chain may move in early and load its weights while this one
+// drains.  With LORA (136 to 194 KB) registers (two blocks' share; 103 a thread
+// for 128 tokens) and shared memory let a block in beside one of the shrink's, to
+// run over x and W while v is computed: 256 tokens of 256 requests, 6144 to 2048
+// at rank 64, 36.0 -> 34.3 us.
 #pragma once
 
 #include "ftm_dense.cuh"
@@ -61,11 +62,9 @@ struct ProjShape {
   static constexpr int kBlocks = LORA && BN < 128 ? 2 : 1;             // that registers are held to
   static constexpr int kThreads = 64 + 32 * kDrain;
   static constexpr size_t kSmem = 1024 + static_cast<size_t>(kStages) * kStage + kLoraRing * kGroup * kBuf + kRed;
+  static constexpr int kPerSm = 2 * (kSmem + 2048) <= 228 * 1024 ? 2 : 1;   // blocks that shared memory lets in
+  static_assert(LORA || BN > 64 || kPerSm == 2, "the next launch moves in beside this one");
 };
-
-__device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
-  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
-}
 
 __device__ __forceinline__ void st_cluster_f32x4(uint32_t addr, const float* f) {
   st_cluster_v4(addr, f[0], f[1], f[2], f[3]);
@@ -379,10 +378,9 @@ cudaError_t launch_proj_bn(const ProjArgs& a, cudaStream_t st) {
     (void)cudaGetLastError();
     return f;
   }();
-  constexpr int kPerSm = 2 * (S::kSmem + 2048) <= 228 * 1024 ? 2 : 1;
   int ks = 1;
   for (int c = 2; c <= 8 && c <= a.kb && c * tiles <= num_sms(); ++c)
-    if (tiles <= kPerSm * fit.n[c]) ks = c;
+    if (tiles <= S::kPerSm * fit.n[c]) ks = c;
   cfg.gridDim = dim3(ks, nt, mt);
   attr[0].val.clusterDim.x = ks;
   cfg.numAttrs = 2;
