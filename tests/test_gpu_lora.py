@@ -531,3 +531,13 @@ def test_split_over_pairs_captured_strided_and_on_two_streams(T, d_in, d_out):
     other.done()
     other.check()
     assert torch.equal(y, keep)
+
+
+@pytest.mark.parametrize("T,d_in,d_out,n,rank,mix", [(9, 4096, 9728, 4, 16, "distinct"), (32, 512, 9600, 32, 16, "distinct"),
+                                                     (64, 4096, 9728, 6, 40, "mixed"), (128, 264, 10248, 3, 128, "runs"),
+                                                     (5, 520, 20480, 5, 16, "mixed")])
+def test_few_tokens_on_wide_projections(T, d_in, d_out, n, rank, mix):
+    m = Linear(T, d_in, d_out, n, rank, mix, seed=T)
+    m.run()
+    m.done()
+    m.check()
