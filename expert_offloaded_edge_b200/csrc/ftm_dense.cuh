@@ -644,13 +644,10 @@ inline bool dense_store_map(CUtensorMap* m, void* base, uint64_t cols, uint64_t 
 
 // Map of a half slot: box {32 columns, 32 rows}, 64-byte swizzle.
 inline bool dense_half_map(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows, uint64_t pitch_bytes) {
-  EncodeTiledFn enc = get_encode_fn();
-  if (!enc) return false;
   const cuuint64_t dims[2] = {cols, rows}, strides[1] = {pitch_bytes};
-  const cuuint32_t box[2] = {32, 32}, es[2] = {1, 1};
-  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, es,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  const cuuint32_t box[2] = {32, 32};
+  return encode_map(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_64B,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
 }
 
 // A problem's sizes: out_cols output columns per tile.

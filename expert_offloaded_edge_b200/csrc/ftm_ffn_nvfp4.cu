@@ -1183,17 +1183,10 @@ static bool nvfp4_pair_applicable(int P, int E) { return (P + E - 1) / E >= 192;
 // dims {256, rows[, slots]}, box {256, box_rows[, 1]}.
 static bool make_map_rows256(CUtensorMap* m, const void* base, uint64_t bytes, uint64_t slots, uint64_t slot_pitch,
                              uint32_t box_rows) {
-  EncodeTiledFn enc = get_encode_fn();
-  if (!enc) return false;
-  cuuint64_t dims[3] = {256, bytes / 256, slots};
-  cuuint64_t strides[2] = {256, slot_pitch};
-  cuuint32_t box[3] = {256, box_rows, 1};
-  cuuint32_t es[3] = {1, 1, 1};
-  const cuuint32_t rank = slots > 0 ? 3 : 2;
-  CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, rank, const_cast<void*>(base), dims, strides, box, es,
-                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS;
+  const cuuint64_t dims[3] = {256, bytes / 256, slots}, strides[2] = {256, slot_pitch};
+  const cuuint32_t box[3] = {256, box_rows, 1};
+  return encode_map(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, slots > 0 ? 3 : 2, base, dims, strides, box,
+                    CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
 }
 
 template <bool GATED, bool MX>

@@ -246,16 +246,30 @@ typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t,
                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
-inline EncodeTiledFn get_encode_fn() {
-  static EncodeTiledFn fn = nullptr;
-  if (!fn) {
+// cuTensorMapEncodeTiled for unit element strides and no interleave.  A driver
+// call wants a context that is current to the host thread; a thread that has made
+// no CUDA call of its own yet has none (the runtime makes the device's primary
+// context current when it first needs it), and gets it here.
+inline bool encode_map(CUtensorMap* m, CUtensorMapDataType dt, uint32_t rank, const void* base, const cuuint64_t* dims,
+                       const cuuint64_t* strides, const cuuint32_t* box, CUtensorMapSwizzle swizzle,
+                       CUtensorMapL2promotion promotion) {
+  static const EncodeTiledFn fn = [] {
     void* p = nullptr;
     cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<EncodeTiledFn>(p);
-  }
-  return fn;
+    const bool found = cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
+                       q == cudaDriverEntryPointSuccess;
+    return found ? reinterpret_cast<EncodeTiledFn>(p) : nullptr;
+  }();
+  if (!fn) return false;
+  const cuuint32_t ones[5] = {1, 1, 1, 1, 1};
+  auto encode = [&] {
+    return fn(m, dt, rank, const_cast<void*>(base), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+              promotion, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  };
+  CUresult r = encode();
+  int dev = 0;
+  if (r == CUDA_ERROR_INVALID_CONTEXT && cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess) r = encode();
+  return r == CUDA_SUCCESS;
 }
 
 // K-major map with a 128-byte inner box and 128-byte swizzle: dims {K, rows[, slots]}
@@ -263,16 +277,10 @@ inline EncodeTiledFn get_encode_fn() {
 inline bool make_map_sw128(CUtensorMap* m, CUtensorMapDataType dt, uint32_t elt_bytes, const void* base, uint64_t K,
                            uint64_t rows, uint64_t row_pitch, uint64_t slots, uint64_t slot_pitch,
                            uint32_t box_rows) {
-  EncodeTiledFn enc = get_encode_fn();
-  if (!enc) return false;
-  cuuint64_t dims[3] = {K, rows, slots};
-  cuuint64_t strides[2] = {row_pitch, slot_pitch};
-  cuuint32_t box[3] = {128u / elt_bytes, box_rows, 1};
-  cuuint32_t es[3] = {1, 1, 1};
-  const cuuint32_t rank = slots > 0 ? 3 : 2;
-  CUresult r = enc(m, dt, rank, const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS;
+  const cuuint64_t dims[3] = {K, rows, slots}, strides[2] = {row_pitch, slot_pitch};
+  const cuuint32_t box[3] = {128u / elt_bytes, box_rows, 1};
+  return encode_map(m, dt, slots > 0 ? 3 : 2, base, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
 }
 
 inline int num_sms() {
