@@ -1,5 +1,8 @@
-"""The dense operators called as programs call them: from new host threads, several of
-them at once."""
+"""The dense operators called as programs call them: inputs written just before, the first call of a process captured,
+several host threads at once, memory of torch's expandable segments."""
+import os
+import subprocess
+import sys
 import threading
 
 import pytest
@@ -7,9 +10,98 @@ import torch
 
 import expert_offloaded_edge_b200 as ftm
 from tests.test_gpu_gated_ffn import Block, normal
-from tests.test_gpu_lora import Linear
+from tests.test_gpu_lora import Linear, adapters_of
 
 pytestmark = pytest.mark.gpu
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+
+@pytest.mark.parametrize("T,d,I", [(1, 512, 384), (12, 256, 640), (40, 512, 384), (200, 384, 256), (1270, 2176, 512), (9000, 384, 640)])
+def test_the_block_reads_what_was_written_just_before(T, d, I):
+    """Weights, x and dy change in the same stream before every call; launches that start early never see the old ones."""
+    b = Block(T, d, I)
+    sets = [(normal(s, T, d), normal(s + 1, 3 * I * d, std=0.05), normal(s + 2, T, d)) for s in (60, 70, 80)]
+    outs = (b.y, b.pre, b.dx, b.dbank)
+
+    def call(k):
+        for to, src in zip((b.x, b.bank, b.dy), sets[k]):
+            to.copy_(src)
+        b.forward()
+        b.backward()
+        return [t.clone() for t in outs]
+
+    want = []
+    for k in range(3):
+        want.append(call(k))
+        b.done()
+        b.check_forward()
+        b.check_backward()
+    wrong = torch.zeros((), dtype=torch.int64, device="cuda")
+    for i in range(150):
+        for p, q in zip(call(i % 3), want[i % 3]):
+            wrong += (p != q).any()
+    b.done()
+    assert int(wrong) == 0
+
+
+@pytest.mark.parametrize("T,d_in,d_out,rank", [(3, 512, 384, 16), (12, 520, 384, 24), (200, 512, 640, 16), (640, 520, 2048, 40),
+                                               (2500, 264, 2048, 16)])
+def test_the_projection_reads_what_was_written_just_before(T, d_in, d_out, rank):
+    m = Linear(T, d_in, d_out, 5, rank, "mixed")
+    sets = [(normal(s, T, d_in), normal(s + 1, d_out, d_in, std=0.1), normal(s + 2, 5, rank, d_in, std=0.1),
+             normal(s + 3, 5, d_out, rank, std=0.3), adapters_of(T, 5, mix, s)) for s, mix in ((60, "mixed"), (70, "distinct"), (80, "runs"))]
+
+    def call(k):
+        for to, src in zip((m.x, m.w, m.a, m.b, m.ids), sets[k]):
+            to.copy_(src)
+        m.run()
+        return m.y.clone()
+
+    want = []
+    for k in range(3):
+        want.append(call(k))
+        m.done()
+        m.check()
+    wrong = torch.zeros((), dtype=torch.int64, device="cuda")
+    for i in range(150):
+        wrong += (call(i % 3) != want[i % 3]).any()
+    m.done()
+    assert int(wrong) == 0
+
+
+CHILD = """
+import torch
+from tests.test_gpu_gated_ffn import Block
+from tests.test_gpu_lora import Linear
+blocks = [Block(T, d, I, act) for T, d, I, act in ((4, 256, 128, "silu"), (40, 256, 128, "gelu"), (1270, 2176, 512, "silu"), (5000, 256, 128, "gelu"))]
+linears = [Linear(T, 512, do, 5, 16, "mixed") for T, do in ((3, 256), (40, 256), (640, 2048), (2500, 2048))]
+torch.cuda.synchronize()
+def calls():
+    for b in blocks:
+        b.forward()
+        b.backward()
+    for m in linears:
+        m.run()
+{body}
+for b in blocks:
+    b.done()
+    b.check_forward()
+    b.check_backward()
+for m in linears:
+    m.done()
+    m.check()
+print("child done")
+"""
+
+
+@pytest.mark.parametrize("body,env", [
+    ("g = torch.cuda.CUDAGraph()\nwith torch.cuda.graph(g):\n    calls()\ng.replay()", {}),       # nothing of the library ran before
+    ("calls()", {"PYTORCH_CUDA_ALLOC_CONF": "expandable_segments:True"})])
+def test_first_calls_of_a_process(body, env):
+    p = subprocess.run([sys.executable, "-c", CHILD.replace("{body}", body)], cwd=ROOT, env={**os.environ, **env},
+                       capture_output=True, text=True, timeout=240)
+    assert p.returncode == 0 and "child done" in p.stdout, p.stdout[-2000:] + p.stderr[-2000:]
 
 
 def in_a_new_thread(f):
