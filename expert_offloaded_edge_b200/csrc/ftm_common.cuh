@@ -35,8 +35,30 @@ __device__ __forceinline__ uint64_t globaltimer() {
 // anything the predecessor wrote (pdl_wait), and lets its successor launch
 // early (pdl_trigger) so the successor's launch and prologue overlap this
 // kernel's tail.  Both are no-ops for a kernel launched without the attribute.
+//
+// A kernel that begins to read before its own pdl_wait (an `early` launch, and the
+// projection behind the adapters' shrink) reads only what was complete before it
+// started: the launch before it waited for that in every block before its
+// pdl_trigger, or was itself started so, and the last of those triggers starts
+// this one.  pdl_wait promises visibility to the grid that waits; the grid behind
+// it relies on what one grid has been shown being in L2, where every SM meets it.
+// So it reads by TMA or with ld_early, not through an SM's own L1.  What the launch
+// before writes is read after pdl_wait alone, and every early kernel waits before
+// it ends, so that its end still stands for the end of all before it.
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+// Loads from L2 for what is read before the wait, in program order with it (a plain
+// load or an intrinsic may be moved behind it).
+__device__ __forceinline__ int32_t ld_early(const int32_t* p) {
+  int32_t v;
+  asm volatile("ld.global.cg.s32 %0, [%1];" : "=r"(v) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ uint4 ld_early(const uint4* p) {
+  uint4 v;
+  asm volatile("ld.global.cg.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
 
 // Host count of kernel launches enqueued by the library (read by
 // ftm_kernel_launches); every launch site passes its result through here.

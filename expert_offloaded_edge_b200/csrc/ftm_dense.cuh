@@ -528,7 +528,7 @@ __global__ void __launch_bounds__(DenseShape<EPI, LORA>::kThreads, 1)
       for (int i = 0, t; ok && (t = dense_tile_at(g, pair, np, i)) >= 0; ++i) {
         const DenseTile ti = dense_decode(g, t);
         const int m0 = ti.m * kDTileM;
-        const int i0 = lora_id(L.ids, L.T, L.n, m0 + e), i1 = lora_id(L.ids, L.T, L.n, m0 + 128 + e);
+        const int i0 = lora_id<true>(L.ids, L.T, L.n, m0 + e), i1 = lora_id<true>(L.ids, L.T, L.n, m0 + 128 + e);
         int at;
         const int nl = lora_list<256>(ls, e, i0, i1, static_cast<int>(rank), at);
         auto send = [&](uint32_t slot, uint32_t n, bool last, bool bad) {

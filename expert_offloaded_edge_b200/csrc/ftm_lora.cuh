@@ -61,10 +61,11 @@ __device__ __forceinline__ bool feed_all(bool p) {
 }
 
 // The adapter of token t: -1 outside the batch, and for an id out of range
-// (reported in the device status word).
+// (reported in the device status word).  EARLY: read before the launch's wait.
+template <bool EARLY = false>
 __device__ __forceinline__ int lora_id(const int32_t* ids, int T, int n, int t) {
   if (t >= T) return -1;
-  const int id = ids[t];
+  const int id = EARLY ? ld_early(ids + t) : ids[t];
   if (id >= -1 && id < n) return id;
   report_bad_index();
   return -1;

@@ -42,7 +42,7 @@ __global__ void __launch_bounds__(kTokenThreads, 2) lora_token_kernel(const Toke
 
   const uint16_t* const xr[1] = {g < p.T ? p.x + g * p.ldx : nullptr};
   auto dot = [&](const uint16_t* r0, const uint16_t* r1) {
-    token_dot<1>(r0, r1, xr, p.K, warp, kTokenHalf, red[half][warp], [] {});
+    token_dot<1, false>(r0, r1, xr, p.K, warp, kTokenHalf, red[half][warp], [] {});
   };
   auto sum = [&](int h, int t, int row) {
     float f = 0.f;

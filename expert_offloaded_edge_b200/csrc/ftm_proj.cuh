@@ -198,7 +198,7 @@ __global__ void __launch_bounds__(ProjShape<BN, LORA>::kThreads, ProjShape<BN, L
     if constexpr (LORA) {
       if (warp < 6) {
         const int e = threadIdx.x - 64;
-        const int i0 = e < BN ? lora_id(a.lora.ids, a.T, a.lora.n, n0 + e) : -1;
+        const int i0 = e < BN ? lora_id<true>(a.lora.ids, a.T, a.lora.n, n0 + e) : -1;
         int at;
         const int nl = lora_list<128>(ls, e, i0, -1, 0, at);
         if (e == 0) {

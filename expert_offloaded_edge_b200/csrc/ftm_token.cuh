@@ -11,7 +11,7 @@
 // Every block reads all tokens: beyond 16 that is more than its weights, and for
 // 16 of large weights as many bytes from L2.  The gated block in a replayed
 // graph, here and on ftm_proj.cuh, us:
-//    1 token,  2048 x 768     3.8   7.8      16 tokens,  2048 x 768     5.5   8.2
+//    1 token,  2048 x 768     3.6   7.8      16 tokens,  2048 x 768     5.5   8.2
 //    1 token,  4096 x 2048   11.5  16.0      16 tokens,  4096 x 2048   14.9  16.6
 //    8 tokens, 6144 x 2048   17.5  20.5      16 tokens,  6144 x 2048   21.7  20.9
 //    1 token,  6144 x 256     6.4   9.4      16 tokens,  6144 x 256     9.6   9.9
@@ -38,14 +38,18 @@ __device__ __forceinline__ void mma_bf16_16816(float* c, uint32_t a0, uint32_t a
 // The products of a tile's 16 rows with NT tiles of tokens over one of `warps`
 // warps' share of K, into to[token * kTokenPitch + row].  r0, r1: rows lane / 4
 // and that + 8 of the tile; xr: token lane / 4 of each tile (NULL: zeros).
-// ready() is called once, before the tokens are first read.
-template <int NT, typename Ready>
+// ready() is called once, before the tokens are first read.  EARLY: the weights
+// are read before the launch's wait (ftm_common.cuh).
+template <int NT, bool EARLY, typename Ready>
 __device__ __forceinline__ void token_dot(const uint16_t* r0, const uint16_t* r1, const uint16_t* const (&xr)[NT], int K, int warp,
                                           int warps, float* to, Ready ready) {
   constexpr int U = 2;                                   // steps at a time
   const int lane = threadIdx.x % 32, g = lane >> 2, tq = lane & 3;
   const int steps = (K + 31) / 32;
   const uint4 zero = make_uint4(0, 0, 0, 0);
+  auto weight = [](const uint16_t* p) {
+    return EARLY ? ld_early(reinterpret_cast<const uint4*>(p)) : __ldg(reinterpret_cast<const uint4*>(p));
+  };
   float acc[NT][4] = {};
   bool waited = false;
   // two neighbouring steps (128 bytes of a row) are a warp's, then the next warp's
@@ -55,8 +59,8 @@ __device__ __forceinline__ void token_dot(const uint16_t* r0, const uint16_t* r1
     for (int u = 0; u < U; ++u) {
       const int k = (c + u) * 32 + tq * 8;
       const bool in = k < K;
-      a0[u] = in && r0 ? __ldg(reinterpret_cast<const uint4*>(r0 + k)) : zero;
-      a1[u] = in && r1 ? __ldg(reinterpret_cast<const uint4*>(r1 + k)) : zero;
+      a0[u] = in && r0 ? weight(r0 + k) : zero;
+      a1[u] = in && r1 ? weight(r1 + k) : zero;
     }
     if (!waited) ready();
     waited = true;
@@ -107,7 +111,7 @@ __global__ void __launch_bounds__(kTokenThreads, 2) token_product_kernel(const T
     const int t = j * kTokenTile + g;
     xr[j] = t < p.T ? p.x + static_cast<size_t>(t) * p.K : nullptr;
   }
-  token_dot<NT>(in0 ? p.a + static_cast<size_t>(r0) * p.K : nullptr, in1 ? p.a + static_cast<size_t>(r1) * p.K : nullptr,
+  token_dot<NT, !GATED>(in0 ? p.a + static_cast<size_t>(r0) * p.K : nullptr, in1 ? p.a + static_cast<size_t>(r1) * p.K : nullptr,
                 xr, p.K, warp, kWarps, red[warp], [&] {
                   if (p.early) ready();
                 });

@@ -172,3 +172,41 @@ def test_host_threads_at_once():
             w.check_backward()
         else:
             w.check()
+
+
+@pytest.mark.parametrize("T,d,I", [(1, 2048, 768), (8, 512, 256), (12, 2048, 128), (40, 512, 256)])
+@pytest.mark.parametrize("graph", [False, True])
+def test_weights_that_the_launch_before_wrote(T, d, I, graph):
+    """The down weights are the output of an adapter projection right in front of the block, so that between their
+    writing and the down launch, which reads them early, there are only launches that start early themselves."""
+    b, n = Block(T, d, I), 8
+    w_d = b.bank[2 * I * d:].view(d, I)
+    m = Linear(d, 128, I, 2, 8, "none", std=0.1)
+    xs = [normal(10 + i, d, 128, std=0.05) for i in range(n)]
+    ys = torch.zeros(n, T, d, dtype=torch.bfloat16, device="cuda")
+
+    def chain():
+        for i in range(n):
+            ftm.ftm_lora_linear(m.D, xs[i], d, m.w, m.a, m.b, None, m.ids, w_d, m.ws, m.ws.numel())
+            b.forward(pre=False, y=ys[i])
+
+    want = []
+    for i in range(n):
+        ftm.ftm_lora_linear(m.D, xs[i], d, m.w, m.a, m.b, None, m.ids, w_d, m.ws, m.ws.numel())
+        torch.cuda.synchronize()
+        b.forward(pre=False)
+        b.done()
+        b.check_forward(pre=False)
+        want.append(b.y[:T].clone())
+    if graph:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            chain()
+        call = g.replay
+    else:
+        call = chain
+    for _ in range(30):
+        ys.zero_()
+        call()
+        b.done()
+        assert torch.equal(ys, torch.stack(want))
