@@ -11,7 +11,7 @@
 // Every block reads all tokens: beyond 16 that is more than its weights, and for
 // 16 of large weights as many bytes from L2.  The gated block in a replayed
 // graph, here and on ftm_proj.cuh, us:
-//    1 token,  2048 x 768     3.6   7.8      16 tokens,  2048 x 768     5.5   8.2
+//    1 token,  2048 x 768     4.2   7.8      16 tokens,  2048 x 768     5.5   8.2
 //    1 token,  4096 x 2048   11.5  16.0      16 tokens,  4096 x 2048   14.9  16.6
 //    8 tokens, 6144 x 2048   17.5  20.5      16 tokens,  6144 x 2048   21.7  20.9
 //    1 token,  6144 x 256     6.4   9.4      16 tokens,  6144 x 256     9.6   9.9

@@ -483,6 +483,8 @@ typedef enum ftm_act {
  *   pre        device bf16 [T][2I] or NULL: receives g (columns 0..I-1) and u
  *              (I..2I-1) for ftm_gated_ffn_backward.  y does not depend on it
  *   workspace  device, >= ftm_gated_ffn_workspace_bytes(L, T) bytes, 256-aligned
+ * Sums are fp32; h is rounded to bf16 between the two products (y is off by about
+ * 0.24% root mean square, a plain bf16 rounding of the exact one by 0.17%).
  * T = 0 is a no-op.  Device pointers are 16-byte aligned and lie on the current
  * device, where `stream` belongs; anything else is refused.  No host
  * synchronisation; the launches may be captured into a CUDA graph.  Calls that
