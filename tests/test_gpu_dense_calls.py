@@ -210,3 +210,24 @@ def test_weights_that_the_launch_before_wrote(T, d, I, graph):
         call()
         b.done()
         assert torch.equal(ys, torch.stack(want))
+
+
+@pytest.mark.parametrize("T,d,I", [(3, 1 << 20, 128), (40, 1 << 20, 128), (3, 128, 1 << 20), (40, 128, 1 << 20)])
+def test_the_block_at_the_largest_widths(T, d, I):
+    b = Block(T, d, I, "silu", seed=T)
+    b.bank.mul_(0.1)
+    b.forward()
+    b.backward()
+    b.done()
+    b.check_forward()
+    b.check_backward()
+
+
+@pytest.mark.parametrize("T,d_in,d_out,n,rank", [(2, 1 << 20, 64, 2, 8), (40, 1 << 20, 64, 2, 24), (2, 64, 1 << 20, 2, 8),
+                                                 (40, 64, 1 << 20, 3, 16), (70, 64, 128, 65536, 8), (3, 64, 128, 65536, 8)])
+def test_adapters_at_the_largest_sizes(T, d_in, d_out, n, rank):
+    m = Linear(T, d_in, d_out, n, rank, "distinct", seed=T)
+    m.ids[0] = n - 1
+    m.run()
+    m.done()
+    m.check()
